@@ -405,6 +405,166 @@ int santa_read_device_error(unsigned int *error_flags, santa_stream_t stream, un
 /* A static, human-readable name for a status code. */
 const char *santa_status_string(int status);
 
+/* ======================================================================
+ * The operators around the attention of a decode step
+ * ======================================================================
+ * One step of a serving loop: santa_page_plan gives every new token a cache row
+ * (block tables and slot maps from the requests' lengths), santa_norm_rope
+ * normalises and rotates the step's queries and keys and writes the keys and
+ * values into those rows, and an attention entry point reads the cache:
+ * santa_decode_prop_paged above, or, exactly, santa_decode_window (a sliding
+ * window behind a few first tokens) and santa_decode_kv4 (a cache held in 4 bits).
+ *
+ * The conventions above hold (ownership, asynchrony, host checks before
+ * anything is enqueued, SANTA_ERR_* bits for device-side input errors, no
+ * traps), with these differences: Hq / Hkv may be any whole number from 1 to 8;
+ * problem fields that a call does not name (tile, S, and for the token-wise
+ * calls batch, max_len) are ignored.
+ */
+
+/* More bits of the device error word. */
+enum {
+    SANTA_ERR_SLOT = 16u,     /* a slot >= total_tokens: that token's row is not written (read: zeros) */
+    SANTA_ERR_PAGES = 32u,    /* page plan: a sequence that does not fit (see santa_page_plan) */
+    SANTA_ERR_POSITION = 64u, /* a position outside [0, max_pos): clamped into it */
+    SANTA_ERR_VALUE = 128u    /* 4-bit append: a NaN (stored as 0) or a value beyond +-65504 (clamped) */
+};
+
+/*
+ * Block tables and slot maps from request lengths.  Sequence b holds kv_lens[b]
+ * tokens in the pages page_table[b][0 .. ceil(kv_lens[b] / page_size)) and is to
+ * receive new_lens[b] more (0: none).  The pages it lacks are taken from
+ * free_pages in order, sequence by sequence, and entered into its row of
+ * page_table (no other entry is written); its new tokens get the positions
+ * kv_lens[b] .. kv_lens[b] + new_lens[b] - 1 and the cache rows of those.
+ *   kv_lens, new_lens  device [batch] int32
+ *   page_table         device [batch][max_pages] int32, updated in place
+ *   free_pages         device [num_free] int32, distinct pages no sequence holds
+ *   slot_map           device [max_tokens] int64: row of each new token, the tokens
+ *                      of sequence 0 first, then those of sequence 1, ...
+ *   positions          device [max_tokens] int32: their positions
+ *   lens_out           device [batch] int32: the new lengths; not kv_lens itself
+ *                      (a call that is repeated gives the same answer)
+ *   counts             device [2] int32: pages taken, tokens placed (rows that
+ *                      got a slot)
+ * Rows of slot_map behind the last token are -1 and their positions 0, so that a
+ * step captured for max_tokens rows runs on fewer.  A sequence that does not fit
+ * -- a negative length, more than max_pages pages, tokens beyond max_tokens, or
+ * free_pages used up (from the first that does not find its pages on, every one
+ * that needs a page) -- takes no page and keeps its length (a negative one: 0), its
+ * rows of slot_map are -1 (positions 0), and SANTA_ERR_PAGES is raised; the others
+ * are served as if it had asked for nothing.  (The rows of slot_map are counted with every
+ * max(new_lens, 0).)  A page id outside [0, num_pages) gives slot -1 and raises
+ * SANTA_ERR_INDPTR.  One kernel, no workspace.
+ */
+int santa_page_plan(int batch, int page_size, int max_pages, long long num_pages, const int *kv_lens,
+                    const int *new_lens, int *page_table, const int *free_pages, int num_free, long long *slot_map,
+                    int *positions, int max_tokens, int *lens_out, int *counts, const santa_debug *dbg,
+                    santa_stream_t stream);
+
+/* What santa_norm_rope does to a head's vector x of d elements. */
+typedef struct {
+    const void *q_weight;    /* device [d] dtype; NULL: queries are not normalised */
+    const void *k_weight;    /* device [d] dtype; NULL: keys are not normalised */
+    float eps;               /* y = x / sqrt(mean(x^2) + eps) * weight; eps >= 0 */
+    const float *cos_sin;    /* device [max_pos][rot_dim]: rot_dim / 2 cosines, then as many sines */
+    int max_pos;             /* rows of cos_sin */
+    int rot_dim;             /* elements 0 .. rot_dim - 1 turn: a multiple of 16, 0 < rot_dim <= d */
+    int interleaved;         /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+} santa_rope;
+
+/*
+ * Norms of queries and keys per head and the position rotation, in one pass, with
+ * the write into the cache: for token t at position n the pair (a, b) with cosine c
+ * and sine s of row n of the table becomes (a c - b s, b c + a s), after the norm.
+ * Single precision inside, rounded once to the problem's dtype.
+ *   q          [num_tokens] rows of Hq d elements, q_stride elements apart
+ *   k, v       [num_tokens] rows of Hkv d elements, k_stride / v_stride apart
+ *              (slices of one projection's rows will do; bases 16-byte aligned,
+ *              strides a multiple of 16 bytes and at least a row)
+ *   positions  device [num_tokens] int32
+ *   slot_map   device [num_tokens] int64: the cache row of each token; a negative
+ *              one (padding) leaves the cache as it is; NULL: token t is row t.
+ *              Rows must be distinct: of two tokens with one row either's elements stay
+ *   q_out      [num_tokens][Hq][d]; q itself may be given if its rows are contiguous
+ *   k_cache, v_cache  [total_tokens][Hkv][d], the cache (or the page pools)
+ * q with q_out, k with k_cache and v with v_cache may each be NULL (left out); v is
+ * copied.  Queries of padding tokens are computed like the others.
+ */
+int santa_norm_rope(const santa_problem *p, const santa_rope *r, int num_tokens, const void *q, long long q_stride,
+                    const void *k, long long k_stride, const void *v, long long v_stride, const int *positions,
+                    const long long *slot_map, void *q_out, void *k_cache, void *v_cache, const santa_debug *dbg,
+                    santa_stream_t stream);
+
+/* The keys that a query sees: the last `window` of its sequence and the first
+ * `sinks` (a key that is both counts once).  window = 0: all of them. */
+typedef struct {
+    int window;              /* >= 0 */
+    int sinks;               /* >= 0 */
+} santa_window;
+
+/*
+ * Exact decode attention under a sliding window with sinks: out = sum_i softmax(x)_i
+ * V_i over the keys i < sinks or i >= L_b - window of each sequence, reading no
+ * other key's block of 32.  Arguments as exact_decode; with `pages` (may be NULL) k
+ * and v are page pools and kv_indptr is unused, as in santa_decode_prop_paged.  What
+ * keys outside the window hold (infinities and NaN included) does not matter.  An
+ * empty sequence gives zeros.  Results do not depend on timing: equal calls give
+ * equal bits.
+ * Workspace: santa_split_workspace_size, prepared once by santa_split_workspace_init;
+ * every call leaves it ready for the next, of santa_decode_window or santa_decode_kv4
+ * on the same problem, and calls that may overlap (two graphs, two streams) need one
+ * each.
+ */
+int santa_decode_window(const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
+                        const void *k, const void *v, const long long *kv_indptr, float *out, void *workspace,
+                        size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream);
+
+/* Bytes of workspace of santa_decode_window and santa_decode_kv4, and its one-time preparation. */
+int santa_split_workspace_size(const santa_problem *p, size_t *bytes);
+int santa_split_workspace_init(const santa_problem *p, void *workspace, size_t workspace_bytes,
+                               santa_stream_t stream);
+
+/*
+ * A K/V cache held in 4 bits: kv4 is [total_tokens][Hkv] records of d + d / 8
+ * bytes, 16-byte aligned as a whole.  A record holds the codes of K (d / 2 bytes:
+ * element i in byte i / 2, the even one in the low half), those of V (d / 2 bytes),
+ * then for K and after that for V the d / 64 pairs (scale, minimum) in fp16 of the
+ * row's groups.  Element i belongs to group (i / 8) mod (d / 64) and stands for
+ * minimum + scale * code.  Rows are addressed as in the other caches (kv_indptr, or
+ * pages of page_size rows).  santa_kv4_size gives the cache's bytes.
+ */
+int santa_kv4_size(const santa_problem *p, size_t *bytes);
+
+/*
+ * Stores tokens into the 4-bit cache: k and v are [num_tokens] rows of Hkv d elements
+ * (problem dtype), k_stride / v_stride elements apart, as for santa_norm_rope;
+ * slot_map as there.  Per group, in single precision: the minimum rounded to fp16,
+ * scale = fp16((max - minimum) * (1/15)), code = round((x - minimum) / scale) to
+ * nearest even, held to 0 .. 15 (scale 0: code 0).  A NaN is stored as 0 and a value
+ * beyond +-65504 as that bound (SANTA_ERR_VALUE).
+ */
+int santa_kv4_append(const santa_problem *p, int num_tokens, const void *k, long long k_stride, const void *v,
+                     long long v_stride, const long long *slot_map, void *kv4, const santa_debug *dbg,
+                     santa_stream_t stream);
+
+/*
+ * Reads rows of the 4-bit cache back: k and v [num_tokens][Hkv][d] in the problem's
+ * dtype (rounded once); either may be NULL.  A negative slot gives zeros.
+ */
+int santa_kv4_read(const santa_problem *p, int num_tokens, const void *kv4, const long long *slot_map, void *k,
+                   void *v, const santa_debug *dbg, santa_stream_t stream);
+
+/*
+ * Exact decode attention over the 4-bit cache: santa_decode_window's arguments with
+ * kv4 for k and v; w may be NULL (all keys).  The problem's dtype is q's.  The
+ * dequantised values enter as they stand (no rounding to 8 or 16 bits); q, the
+ * softmax weights and the sums keep 22 bits or more.
+ */
+int santa_decode_kv4(const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
+                     const void *kv4, const long long *kv_indptr, float *out, void *workspace,
+                     size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

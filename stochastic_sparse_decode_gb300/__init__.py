@@ -22,6 +22,7 @@ OK, INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA_ERROR, DEVICE_CHECK = ra
 F32, BF16 = 0, 1
 MODE_PROP, MODE_FLASH, MODE_EXACT = 0, 1, 2
 ERR_INDPTR, ERR_OFFSET, ERR_TIMEOUT, ERR_WORKSPACE = 1, 2, 4, 8
+ERR_SLOT, ERR_PAGES, ERR_POSITION, ERR_VALUE = 16, 32, 64, 128
 
 EXPORTS = (
     "santa_workspace_size",
@@ -40,6 +41,15 @@ EXPORTS = (
     "exact_decode",
     "santa_read_device_error",
     "santa_decode_prop_static_scratch",
+    "santa_page_plan",
+    "santa_norm_rope",
+    "santa_decode_window",
+    "santa_split_workspace_size",
+    "santa_split_workspace_init",
+    "santa_kv4_size",
+    "santa_kv4_append",
+    "santa_kv4_read",
+    "santa_decode_kv4",
     "santa_status_string",
 )
 
@@ -95,6 +105,26 @@ class Pages(ctypes.Structure):
     ]
 
 
+class Rope(ctypes.Structure):
+    """santa_rope"""
+
+    _fields_ = [
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("cos_sin", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int),
+        ("rot_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+    ]
+
+
+class Window(ctypes.Structure):
+    """santa_window"""
+
+    _fields_ = [("window", ctypes.c_int), ("sinks", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -123,6 +153,17 @@ def lib() -> ctypes.CDLL:
         L.santa_decode_prop_paged.argtypes = [P, ctypes.POINTER(Pages), vp, vp, vp, vp, vp, vp, sz, Dp, vp]
         L.exact_decode.argtypes = [P, vp, vp, vp, vp, vp, vp, sz, Dp, vp]
         L.santa_decode_prop_static_scratch.argtypes = [P, vp, vp, vp, vp, vp, vp, Dp, vp]
+        i, ll = ctypes.c_int, ctypes.c_longlong
+        Wp, Gp = ctypes.POINTER(Window), ctypes.POINTER(Pages)
+        L.santa_page_plan.argtypes = [i, i, i, ll, vp, vp, vp, vp, i, vp, vp, i, vp, vp, Dp, vp]
+        L.santa_norm_rope.argtypes = [P, ctypes.POINTER(Rope), i, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, vp, Dp, vp]
+        L.santa_decode_window.argtypes = [P, Wp, Gp, vp, vp, vp, vp, vp, vp, sz, Dp, vp]
+        L.santa_decode_kv4.argtypes = [P, Wp, Gp, vp, vp, vp, vp, vp, sz, Dp, vp]
+        L.santa_split_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+        L.santa_split_workspace_init.argtypes = [P, vp, sz, vp]
+        L.santa_kv4_size.argtypes = [P, ctypes.POINTER(sz)]
+        L.santa_kv4_append.argtypes = [P, i, vp, ll, vp, ll, vp, vp, Dp, vp]
+        L.santa_kv4_read.argtypes = [P, i, vp, vp, vp, vp, Dp, vp]
         L.santa_read_device_error.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint)]
         L.santa_status_string.argtypes = [ctypes.c_int]
         L.santa_status_string.restype = ctypes.c_char_p
@@ -269,6 +310,84 @@ def exact_decode(problem, q, k, v, kv_indptr, out, workspace, debug=None, stream
     """Exact split-KV decode: see santa_decode.h."""
     _call("exact_decode", problem, [_ptr(q), _ptr(k), _ptr(v), _ptr(kv_indptr), _ptr(out)],
           workspace, debug, stream)
+
+
+def _check(name, status):
+    if status != OK:
+        raise SantaError(status, name)
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def split_workspace_size(problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("santa_split_workspace_size", lib().santa_split_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def santa_split_workspace_init(problem, workspace, stream=None):
+    """Prepares a workspace of santa_decode_window / santa_decode_kv4: see santa_decode.h."""
+    _check("santa_split_workspace_init", lib().santa_split_workspace_init(
+        ctypes.byref(problem), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def santa_decode_window(problem, window, q, k, v, kv_indptr, out, workspace, pages=None, debug=None, stream=None):
+    """Exact decode under a sliding window with sinks (window: a Window): see santa_decode.h."""
+    _check("santa_decode_window", lib().santa_decode_window(
+        ctypes.byref(problem), _ref(window), _ref(pages), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_indptr), _ptr(out),
+        _ptr(workspace), _nbytes(workspace), _ref(debug), _stream(stream)))
+
+
+def santa_decode_kv4(problem, window, q, kv4, kv_indptr, out, workspace, pages=None, debug=None, stream=None):
+    """Exact decode over a 4-bit cache (window: a Window or None): see santa_decode.h."""
+    _check("santa_decode_kv4", lib().santa_decode_kv4(
+        ctypes.byref(problem), _ref(window), _ref(pages), _ptr(q), _ptr(kv4), _ptr(kv_indptr), _ptr(out),
+        _ptr(workspace), _nbytes(workspace), _ref(debug), _stream(stream)))
+
+
+def kv4_size(problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("santa_kv4_size", lib().santa_kv4_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def _row_stride(t) -> int:
+    """Elements from one token to the next of a [tokens][heads][d] tensor."""
+    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1] * t.shape[2]))
+
+
+def santa_kv4_append(problem, k, v, slot_map, kv4, debug=None, stream=None):
+    """Stores tokens into the 4-bit cache: see santa_decode.h."""
+    _check("santa_kv4_append", lib().santa_kv4_append(
+        ctypes.byref(problem), int(k.shape[0]), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(slot_map),
+        _ptr(kv4), _ref(debug), _stream(stream)))
+
+
+def santa_kv4_read(problem, num_tokens, kv4, slot_map, k, v, debug=None, stream=None):
+    """Reads rows of the 4-bit cache back: see santa_decode.h."""
+    _check("santa_kv4_read", lib().santa_kv4_read(
+        ctypes.byref(problem), int(num_tokens), _ptr(kv4), _ptr(slot_map), _ptr(k), _ptr(v), _ref(debug),
+        _stream(stream)))
+
+
+def santa_norm_rope(problem, rope, q, k, v, positions, slot_map, q_out, k_cache, v_cache, debug=None, stream=None):
+    """Norms of q and k, the rotation and the cache write (rope: a Rope): see santa_decode.h."""
+    n = next((int(t.shape[0]) for t in (q, k, v) if t is not None), 0)
+    strides = [0 if t is None else _row_stride(t) for t in (q, k, v)]
+    _check("santa_norm_rope", lib().santa_norm_rope(
+        ctypes.byref(problem), ctypes.byref(rope), n, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
+        _ptr(positions), _ptr(slot_map), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ref(debug), _stream(stream)))
+
+
+def santa_page_plan(page_size, num_pages, kv_lens, new_lens, page_table, free_pages, slot_map, positions, lens_out,
+                    counts, debug=None, stream=None):
+    """Block tables and slot maps from request lengths: see santa_decode.h."""
+    _check("santa_page_plan", lib().santa_page_plan(
+        int(kv_lens.numel()), int(page_size), int(page_table.shape[-1]), int(num_pages), _ptr(kv_lens), _ptr(new_lens),
+        _ptr(page_table), _ptr(free_pages), int(free_pages.numel()), _ptr(slot_map), _ptr(positions),
+        int(slot_map.numel()), _ptr(lens_out), _ptr(counts), _ref(debug), _stream(stream)))
 
 
 STATIC_SCRATCH_BYTES = 16 << 20  # SANTA_STATIC_SCRATCH_BYTES

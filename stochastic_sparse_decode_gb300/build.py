@@ -2,7 +2,7 @@
 
     python -m stochastic_sparse_decode_gb300.build [--force] [--ptxas-verbose]
 
-Each ``csrc/*.cu`` is compiled to an object under ``_build/`` in parallel, then
+Each ``csrc/*.cu`` and ``csrc/serving/*.cu`` is compiled to an object under ``_build/`` in parallel, then
 linked into ``libsanta_decode.so`` next to this file (the CUDA runtime is
 linked statically, so the library only needs the driver at run time).
 """
@@ -41,11 +41,12 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "serving", "*.cu")))
 
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+        glob.glob(os.path.join(CSRC, "serving", "*.cuh")) + glob.glob(os.path.join(CSRC, "serving", "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 

@@ -1,0 +1,152 @@
+// santa_page_plan.cu -- block tables and slot maps from request lengths, in one kernel.
+//
+// With have_b = ceil(len_b / ps), need_b = ceil((len_b + new_b) / ps) - have_b and the
+// prefix sums P_b = sum_{b' < b} need_b', T_b = sum_{b' < b} max(new_b', 0):
+//   page_table[b][have_b + i] = free_pages[P_b + i],                  i < need_b
+//   slot_map[T_b + i] = page(b, n / ps) ps + n mod ps,  n = len_b + i,  i < new_b.
+// Every CTA scans the sequences itself, kPlanThreads at a time (two block scans: the
+// token counts, which decide who fits, then the page counts of those that do), so no
+// CTA waits for another and one launch does it all; the CTAs then share the tile's new
+// pages and tokens, each found by a binary search in the tile's prefix sums.  A page
+// that a token lies in is read from the free list itself when it is new, so the table
+// entries that another CTA writes are never read.
+#include "santa_serving.h"
+
+namespace santa {
+
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanCtas = 304;  // two per SM
+
+__device__ __forceinline__ void plan_flag(const PlanParams &p, unsigned bit) {
+    if (p.err) atomicOr(p.err, bit);
+}
+
+// Inclusive scan over the block; every thread also receives the total.
+__device__ __forceinline__ long long block_scan(long long v, long long *scr, long long *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();  // scr may still be read from the scan before
+    if (lane == 31) scr[warp] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const long long s = scr[w];
+        if (w < warp) before += s;
+        all += s;
+    }
+    *total = all;
+    return v + before;
+}
+
+// First i in [0, n) with end[i] > x (n if there is none).
+__device__ __forceinline__ int upper(const long long *end, int n, long long x) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (end[mid] > x)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p) {
+    __shared__ long long scr[kPlanThreads / 32];
+    __shared__ long long s_tok[kPlanThreads], s_page[kPlanThreads];  // inclusive prefix sums of the tile
+    __shared__ int s_len[kPlanThreads], s_have[kPlanThreads];
+    __shared__ int s_ok[kPlanThreads];
+    const int tid = threadIdx.x;
+    const long long me = (long long)blockIdx.x * kPlanThreads + tid, all = (long long)gridDim.x * kPlanThreads;
+    pdl_wait();
+    pdl_launch_dependents();
+    long long tok0 = 0, page0 = 0;  // of the tiles before
+    long long taken = 0, placed = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int len = 0, nw = 0;
+        if (b < p.batch) {
+            len = p.kv_lens[b];
+            nw = p.new_lens[b];
+        }
+        const bool negative = len < 0 || nw < 0;
+        const long long n_tok = nw > 0 ? nw : 0;
+        long long tile_tok, tile_page;
+        const long long tok_end = block_scan(n_tok, scr, &tile_tok);
+        const long long want = ((long long)len + nw + p.page_size - 1) / p.page_size;
+        bool ok = !negative && want <= p.max_pages && (n_tok == 0 || tok0 + tok_end <= p.max_tokens);
+        const int have = negative ? 0 : int(((long long)len + p.page_size - 1) / p.page_size);
+        const long long need = ok ? want - have : 0;
+        const long long page_end = block_scan(need, scr, &tile_page);
+        if (need > 0 && page0 + page_end > p.num_free) ok = false;
+        s_tok[tid] = tok_end;
+        s_page[tid] = page_end;
+        s_len[tid] = len;
+        s_have[tid] = have;
+        s_ok[tid] = ok;
+        if (b < p.batch && (b0 / kPlanThreads) % gridDim.x == blockIdx.x) {
+            p.lens_out[b] = ok ? len + nw : len > 0 ? len : 0;
+            if (!ok) plan_flag(p, SANTA_ERR_PAGES);
+        }
+        long long x;
+        block_scan(ok ? need : 0, scr, &x);  // its barriers also publish the arrays above
+        taken += x;
+        block_scan(ok ? n_tok : 0, scr, &x);
+        placed += x;
+        const int nb = min(kPlanThreads, p.batch - b0);
+        for (long long i = me; i < tile_page; i += all) {
+            const int s = upper(s_page, nb, i);
+            if (!s_ok[s]) continue;
+            const int k = int(i - (s > 0 ? s_page[s - 1] : 0));
+            p.page_table[(size_t)(b0 + s) * p.max_pages + s_have[s] + k] = p.free_pages[page0 + i];
+        }
+        for (long long i = me; i < tile_tok; i += all) {
+            if (tok0 + i >= p.max_tokens) break;
+            const int s = upper(s_tok, nb, i);
+            const long long first = s > 0 ? s_tok[s - 1] : 0;
+            long long slot = -1;
+            int pos = 0;
+            if (s_ok[s]) {
+                pos = s_len[s] + int(i - first);
+                const int pg = pos / p.page_size, fresh = pg - s_have[s];
+                const int id = fresh >= 0 ? p.free_pages[page0 + (s > 0 ? s_page[s - 1] : 0) + fresh]
+                                          : p.page_table[(size_t)(b0 + s) * p.max_pages + pg];
+                if (id >= 0 && id < p.num_pages)
+                    slot = (long long)id * p.page_size + pos % p.page_size;
+                else
+                    plan_flag(p, SANTA_ERR_INDPTR);
+            }
+            p.slot_map[tok0 + i] = slot;
+            p.positions[tok0 + i] = pos;
+        }
+        tok0 += tile_tok;
+        page0 += tile_page;
+        __syncthreads();
+    }
+    for (long long i = tok0 + me; i < p.max_tokens; i += all) {
+        p.slot_map[i] = -1;
+        p.positions[i] = 0;
+    }
+    if (me == 0) {
+        p.counts[0] = int(taken);
+        p.counts[1] = int(placed);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PlanParams &p, cudaStream_t stream) {
+    const int work = p.max_tokens > p.batch ? p.max_tokens : p.batch;
+    int ctas = (work + kPlanThreads * 4 - 1) / (kPlanThreads * 4);
+    ctas = ctas < 1 ? 1 : ctas > kPlanCtas ? kPlanCtas : ctas;
+    return launch_kernel(page_plan_kernel, dim3(unsigned(ctas)), dim3(kPlanThreads), 0, stream, true, 0, false, p);
+}
+
+}  // namespace santa

@@ -1,0 +1,806 @@
+"""The operators around the attention, on the GPU: page plan, norm + rotation, windowed attention, the
+4-bit cache, and a run of them together.
+
+Every operator is compared with a plain implementation in 64 bits (integers: exactly).  Tolerances come from
+the arithmetic: u is the unit of the sums (fp32 2^-24; sums on the tensor cores are counted at 2^-23, because
+they may truncate), a rounding of the output to its type is half a step, torch.finfo(t).eps / 2.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import stochastic_sparse_decode_gb300 as sd
+from stochastic_sparse_decode_gb300.decoder import Decoder, rope_table
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="session", autouse=True)
+def built_library():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from stochastic_sparse_decode_gb300.build import build
+
+    build()
+
+
+def _flags(dbg_word):
+    return sd.santa_read_device_error(dbg_word)
+
+
+def _debug():
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dbg = sd.Debug()
+    dbg.error_flags = word.data_ptr()
+    return dbg, word
+
+
+# ------------------------------------------------------------------------------ page plan
+
+
+def _plan_reference(lens, new, table, free, ps, num_pages, max_tokens):
+    """The definition, token by token."""
+    table = table.copy()
+    max_pages = table.shape[1]
+    slots, pos = np.full(max_tokens, -1, np.int64), np.zeros(max_tokens, np.int32)
+    out, taken, placed, flags, row, out_of_pages = [], 0, 0, 0, 0, False
+    for b, (n, m) in enumerate(zip(lens.tolist(), new.tolist())):
+        rows = max(m, 0)
+        first, row = row, row + rows
+        need = -(-(n + m) // ps) - -(-n // ps)
+        fits = n >= 0 and m >= 0 and -(-(n + m) // ps) <= max_pages and (rows == 0 or row <= max_tokens)
+        if fits and need > 0 and (out_of_pages or taken + need > len(free)):
+            out_of_pages, fits = True, False
+        if not fits:
+            flags |= sd.ERR_PAGES
+            out.append(max(n, 0))
+            continue
+        for i in range(need):
+            table[b, -(-n // ps) + i] = free[taken + i]
+        taken += need
+        placed += rows
+        out.append(n + m)
+        for i in range(m):
+            page = int(table[b, (n + i) // ps])
+            pos[first + i] = n + i
+            if 0 <= page < num_pages:
+                slots[first + i] = page * ps + (n + i) % ps
+            else:
+                flags |= sd.ERR_INDPTR
+    return table, slots, pos, np.array(out, np.int32), np.array([taken, placed], np.int32), flags
+
+
+def _plan_inputs(rng, batch, ps, hi_len, hi_new, spare_pages=4, max_pages=None):
+    lens, new = rng.integers(0, hi_len + 1, batch), rng.integers(0, hi_new + 1, batch)
+    have = -(-lens // ps)
+    need = -(-(lens + new) // ps) - have
+    max_pages = max_pages or int((have + need).max(initial=0)) + 1
+    num_pages = int(have.sum() + need.sum()) + spare_pages
+    ids = rng.permutation(num_pages).astype(np.int32)
+    table = np.full((batch, max_pages), -9, np.int32)
+    at = 0
+    for b in range(batch):
+        table[b, :min(have[b], max_pages)] = ids[at:at + have[b]][:max_pages]
+        at += have[b]
+    return lens.astype(np.int32), new.astype(np.int32), table, ids[at:].copy(), num_pages
+
+
+def _run_plan(lens, new, table, free, ps, num_pages, max_tokens, stream=None):
+    t = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
+    d = [t(lens), t(new), t(table), t(free)]
+    slots = torch.full((max_tokens,), 12345, dtype=torch.int64, device="cuda")
+    pos = torch.full((max_tokens,), 12345, dtype=torch.int32, device="cuda")
+    out = torch.full((len(lens),), 12345, dtype=torch.int32, device="cuda")
+    counts = torch.full((2,), 12345, dtype=torch.int32, device="cuda")
+    dbg, word = _debug()
+    dec = Decoder(1, 1, 1, 64, num_pages * ps, 32, 256, 1, "f32")
+    for _ in range(2):  # a repeated call gives the same answer
+        dec.page_plan(d[0], d[1], d[2], d[3], ps, slots, pos, out, counts, debug=dbg)
+    flags = _flags(word)
+    return [x.cpu().numpy() for x in (d[2], slots, pos, out, counts)] + [flags]
+
+
+def _check_plan(lens, new, table, free, ps, num_pages, max_tokens):
+    want = _plan_reference(lens, new, table, free, ps, num_pages, max_tokens)
+    got = _run_plan(lens, new, table, free, ps, num_pages, max_tokens)
+    for name, a, b in zip(("table", "slots", "positions", "lens", "counts"), got, want):
+        assert np.array_equal(a, b), name
+    assert got[5] == want[5]
+    return want
+
+
+@pytest.mark.parametrize("batch,ps,hi_len,hi_new", [
+    (1, 32, 0, 1), (1, 1, 5, 7), (3, 64, 200, 1), (64, 64, 3000, 1), (255, 7, 30, 40), (256, 32, 0, 100),
+    (257, 128, 500, 33), (1000, 16, 100, 3), (5, 32, 100, 20000), (2, 4096, 9000, 9000), (40, 32, 64, 0),
+])
+def test_page_plan(batch, ps, hi_len, hi_new):
+    rng = np.random.default_rng(batch * 1000 + ps)
+    lens, new, table, free, num_pages = _plan_inputs(rng, batch, ps, hi_len, hi_new)
+    _check_plan(lens, new, table, free, ps, num_pages, int(new.sum()) + 13)
+    if int(new.sum()):
+        _check_plan(lens, new, table, free, ps, num_pages, int(new.sum()))
+
+
+def test_page_plan_refuses_sequences_that_do_not_fit():
+    rng = np.random.default_rng(3)
+    lens, new, table, free, num_pages = _plan_inputs(rng, 300, 32, 200, 100, max_pages=8)
+    lens[7], lens[200], new[11], new[299] = -3, -2**31, -1, -2**31
+    new[20], lens[30], new[31] = 2**31 - 1, 2**31 - 1, 32 * 8  # beyond the table's row, beyond 32 bits
+    total = int(np.maximum(new.astype(np.int64), 0).sum())
+    new[20] = 40
+    rows = int(np.maximum(new, 0).sum())
+    assert total > rows
+    for free_n in (len(free), len(free) // 2, 1, 0):
+        for tokens in (rows + 5, rows // 2, 1):
+            want = _check_plan(lens, new, table, free[:free_n], 32, num_pages, tokens)
+            assert want[5] & sd.ERR_PAGES
+
+
+def test_page_plan_with_more_rows_than_32_bits_asked():
+    lens = np.zeros(4, np.int32)
+    new = np.array([5, 2**31 - 1, 2**31 - 1, 3], np.int32)
+    table = np.full((4, 4), -1, np.int32)
+    got = _run_plan(lens, new, table, np.arange(9, dtype=np.int32), 32, 9, 64)
+    assert got[4].tolist() == [1, 5] and got[3].tolist() == [5, 0, 0, 0] and got[5] == sd.ERR_PAGES
+    assert got[1][:5].tolist() == list(range(5)) and (got[1][5:] == -1).all()
+
+
+def test_page_plan_flags_bad_page_ids():
+    lens, new = np.array([10, 0, 5], np.int32), np.array([3, 4, 2], np.int32)
+    table = np.array([[99, -1], [-1, -1], [1, -1]], np.int32)
+    want = _check_plan(lens, new, table, np.array([-4], np.int32), 32, 4, 9)
+    assert want[5] == sd.ERR_INDPTR and (want[1][:7] == -1).all() and (want[1][7:] >= 0).all()
+
+
+def test_page_plan_of_no_sequence_pads():
+    got = _run_plan(np.zeros(0, np.int32), np.zeros(0, np.int32), np.zeros((0, 3), np.int32), np.zeros(2, np.int32), 32, 4, 7)
+    assert (got[1] == -1).all() and (got[2] == 0).all() and got[4].tolist() == [0, 0]
+
+
+# ------------------------------------------------------------------------------ norm + rotation
+
+
+def _rope_reference(x, w, eps, cs, rot, inter):
+    """(y, bound on |a| + |b| of its pair) in 64 bits; x [T][H][d], cs [T][rot] (cosines, sines)."""
+    x = x.double()
+    if w is not None:
+        x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * w.double()
+    half = rot // 2
+    cos, sin = cs[:, None, :half].double(), cs[:, None, half:].double()
+    y, mag = x.clone(), x.abs()
+    first = slice(0, rot, 2) if inter else slice(0, half)
+    second = slice(1, rot, 2) if inter else slice(half, rot)
+    a, b = x[..., first], x[..., second]
+    y[..., first], y[..., second] = a * cos - b * sin, b * cos + a * sin
+    mag[..., first] = mag[..., second] = a.abs() + b.abs()
+    return y, mag
+
+
+def _close(got, want, mag, what, u=2.0 ** -24):
+    # the sum of squares (its d terms are positive: (8 + 4) u relative after fused multiply-adds in a tree of
+    # 8 + 4 levels), root, division, two products and the rotation's two: 24 u of the pair's magnitude
+    tol = torch.finfo(got.dtype).eps / 2 * want.abs() + 24 * u * mag
+    bad = (got.double() - want).abs() > tol
+    assert not bad.any(), (what, int(bad.sum()), float(((got.double() - want).abs() - tol).max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,hq,hkv,rot,inter,norm,fused", [
+    (1, 4, 1, 1.0, False, True, False), (3, 32, 8, 1.0, False, False, True), (17, 8, 8, 0.5, True, True, True),
+    (200, 6, 2, 0.75, False, True, True), (33, 5, 5, 0.25, True, False, False), (1000, 32, 4, 1.0, True, True, True),
+])
+def test_norm_rope(dtype, d, T, hq, hkv, rot, inter, norm, fused):
+    dt = DT[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    if fused:
+        qkv = rnd(T, hq + 2 * hkv + 1, d).to(dt)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:hq + 2 * hkv]
+    else:
+        q, k, v = (rnd(T, h, d).to(dt) for h in (hq, hkv, hkv))
+    q[0, 0] *= 1e-3  # eps matters there
+    rot = int(rot * d)
+    rows = T + 7
+    cs = rope_table(5000, rot, 10000.0)
+    pos = torch.randint(0, 5000, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    slots = torch.randperm(rows, generator=gen, device="cuda")[:T].contiguous()
+    slots[T // 2] = -1 if T > 1 else slots[0]  # padding
+    qw, kw = ((1 + 0.3 * rnd(d)).to(dt), (1 + 0.3 * rnd(d)).to(dt)) if norm else (None, None)
+    kc, vc = rnd(rows, hkv, d).to(dt), rnd(rows, hkv, d).to(dt)
+    kc0, vc0 = kc.clone(), vc.clone()
+    dec = Decoder(1, hq, hkv, d, rows, rows, 256, 1, dtype)
+    dbg, word = _debug()
+    out = dec.norm_rope(q, k, v, pos, slots, cs, kc, vc, qw, kw, 1e-5, inter, debug=dbg)
+    assert _flags(word) == 0
+    want, mag = _rope_reference(q, qw, 1e-5, cs[pos.long()], rot, inter)
+    _close(out, want, mag, "q")
+    want, mag = _rope_reference(k, kw, 1e-5, cs[pos.long()], rot, inter)
+    live = slots >= 0
+    _close(kc[slots[live]], want[live], mag[live], "k")
+    assert torch.equal(vc[slots[live]], v[live])
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[slots[live]] = False
+    assert torch.equal(kc[rest], kc0[rest]) and torch.equal(vc[rest], vc0[rest])
+
+
+def test_norm_rope_parts_in_place_and_identity_map():
+    """q alone in place, k alone, v alone, and no slot map: each like the whole call."""
+    T, hq, hkv, d = 9, 4, 2, 64
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((T, h, d), generator=gen, device="cuda").bfloat16() for h in (hq, hkv, hkv))
+    cs = rope_table(64, d)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    dec = Decoder(1, hq, hkv, d, T, T, 256, 1, "bf16")
+    kc, vc = torch.zeros_like(k), torch.zeros_like(v)
+    out = dec.norm_rope(q, k, v, pos, None, cs, kc, vc)
+    q2, kc2, vc2 = q.clone(), torch.zeros_like(k), torch.zeros_like(v)
+    assert dec.norm_rope(q2, None, None, pos, None, cs, None, None, out=q2).data_ptr() == q2.data_ptr()
+    dec.norm_rope(None, k, None, pos, None, cs, kc2, None)
+    dec.norm_rope(None, None, v, pos, None, cs, None, vc2)
+    assert torch.equal(out, q2) and torch.equal(kc, kc2) and torch.equal(vc, vc2) and torch.equal(vc, v)
+
+
+def test_norm_rope_bad_positions_and_slots_are_flagged():
+    T, d = 5, 64
+    q = torch.randn((T, 1, d), device="cuda")
+    cs = rope_table(10, d)
+    pos = torch.tensor([0, -1, 10, 9, 2**31 - 1], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([0, 6, 1, -2**40, 2**40], dtype=torch.int64, device="cuda")
+    kc, vc = torch.zeros((6, 1, d), device="cuda"), torch.zeros((6, 1, d), device="cuda")
+    dec = Decoder(1, 1, 1, d, 6, 6, 256, 1, "f32")
+    dbg, word = _debug()
+    out = dec.norm_rope(q, q, q, pos, slots, cs, kc, vc, debug=dbg)
+    assert _flags(word) == sd.ERR_POSITION | sd.ERR_SLOT
+    want, mag = _rope_reference(q, None, 0.0, cs[pos.clamp(0, 9).long()], d, False)
+    _close(out, want, mag, "q")
+    assert torch.equal(vc[0], q[0]) and torch.equal(vc[1], q[2]) and not vc[2:].any()
+
+
+def test_norm_rope_keeps_special_values_to_their_pairs():
+    """An infinity or NaN reaches its own pair only (no norm), never the elements behind rot_dim or another head."""
+    q = torch.randn((2, 3, 64), device="cuda")
+    q[0, 1, 3], q[1, 2, 40], q[1, 0, 63] = math.inf, math.nan, math.inf
+    cs = rope_table(10, 32)
+    pos = torch.tensor([3, 4], dtype=torch.int32, device="cuda")
+    dec = Decoder(1, 3, 3, 64, 2, 2, 256, 1, "f32")
+    out = dec.norm_rope(q, None, None, pos, None, cs, None, None)
+    bad = ~torch.isfinite(out)
+    want = torch.zeros_like(bad)
+    want[0, 1, 3] = want[0, 1, 19] = want[1, 2, 40] = want[1, 0, 63] = True
+    assert torch.equal(bad, want) and out[1, 0, 63] == math.inf
+
+
+# ------------------------------------------------------------------------------ attention
+
+
+def _attention_reference(q, k, v, scale, u):
+    """Exact output of one KV head's group and its error bound; q [G][d], k, v [n][d] in 64 bits."""
+    x = q @ k.T * scale
+    m = x.amax(-1, keepdim=True)
+    p = torch.softmax(x, -1)
+    d, n = k.shape[1], k.shape[0]
+    # logit: d products and sums; exponential: its argument's roundings and 4 units of the function; the sums:
+    # a chain of at most n / 32 blocks of 32 keys, then parts (64 levels allowed)
+    dx = (d + 8) * u * (q.abs() @ k.abs().T) * scale + 4 * u * (x - m).abs() + 8 * u
+    chain = (n / 32 + 96) * u
+    dz = (p * dx).sum(-1, keepdim=True)
+    tol = (p * (dx + dz)) @ v.abs() + 2 * chain * (p @ v.abs())
+    return p @ v, tol
+
+
+def _seen(n, window, sinks):
+    return [i for i in range(n) if i < sinks or window == 0 or i >= n - window]
+
+
+def _make_cache(lens, hkv, d, dt, page, gen, poison):
+    """Keys and values of each sequence, laid out contiguously or in shuffled pages amid `poison`."""
+    kv = [[torch.randn((n, hkv, d), generator=gen, device="cuda").to(dt) for n in lens] for _ in range(2)]
+    B = len(lens)
+    if not page:
+        rows = sum(lens) + 3
+        pools = [torch.full((rows, hkv, d), poison, device="cuda", dtype=dt) for _ in range(2)]
+        start = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+        where = [torch.arange(start[b], start[b + 1], device="cuda") for b in range(B)]
+        addr = dict(indptr=torch.from_numpy(start).cuda())
+    else:
+        have = [-(-n // page) for n in lens]
+        num = sum(have) + 2
+        rows = num * page
+        pools = [torch.full((rows, hkv, d), poison, device="cuda", dtype=dt) for _ in range(2)]
+        ids = torch.randperm(num, generator=gen, device="cuda").cpu().numpy()
+        table = np.full((B, max(have) + 1), -3, np.int32)
+        at, where = 0, []
+        for b, n in enumerate(lens):
+            table[b, :have[b]] = ids[at:at + have[b]]
+            at += have[b]
+            i = np.arange(n)
+            where.append(torch.from_numpy(table[b, i // page].astype(np.int64) * page + i % page).cuda())
+        addr = dict(table=torch.from_numpy(table).cuda(), lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    for pool, x in zip(pools, kv):
+        for b in range(B):
+            pool[where[b]] = x[b]
+    return pools, kv, where, addr, rows
+
+
+def _values64(rec, d):
+    """K and V in 64 bits of 4-bit records [..][d + d / 8]."""
+    i = torch.arange(d, device=rec.device)
+    out = []
+    for which in range(2):
+        codes = rec[..., which * (d // 2):(which + 1) * (d // 2)].long()
+        n = ((codes[..., i // 2] >> (4 * (i % 2))) & 15).double()
+        at = d + which * (d // 16)
+        p = rec[..., at:at + d // 16].contiguous().view(torch.float16).double()
+        g = (i // 8) % (d // 64)
+        out.append(p[..., 2 * g + 1] + p[..., 2 * g] * n)
+    return out
+
+
+def _run_attention(kind, dec, q, pools, addr, page, window, sinks, debug=None, out=None):
+    if kind == "window":
+        if page:
+            return dec.window_paged(q, *pools, addr["table"], addr["lens"], page, window, sinks, out=out, debug=debug)
+        return dec.window(q, *pools, addr["indptr"], window, sinks, out=out, debug=debug)
+    if page:
+        return dec.kv4_paged(q, pools[0], addr["table"], addr["lens"], page, window, sinks, out=out, debug=debug)
+    return dec.kv4(q, pools[0], addr["indptr"], window, sinks, out=out, debug=debug)
+
+
+def _attention_case(kind, dtype, d, hkv, g, lens, window, sinks, page, seed=0, poison=math.nan, q_scale=1.0, k_shift=0.0):
+    dt = DT[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    pools, kv, where, addr, rows = _make_cache(lens, hkv, d, dt, page, gen, poison)
+    if k_shift:
+        for b in range(len(lens)):
+            kv[0][b] = (kv[0][b].float() + k_shift).to(dt)
+            pools[0][where[b]] = kv[0][b]
+    q = (torch.randn((len(lens), hkv * g, d), generator=gen, device="cuda") * q_scale).to(dt)
+    dec = Decoder(len(lens), hkv * g, hkv, d, rows, max(max(lens), 1), 256, 1, dtype)
+    if kind == "kv4":
+        cache = torch.full((rows, hkv, d + d // 8), 0xFF, dtype=torch.uint8, device="cuda")  # NaN scales outside
+        for b in range(len(lens)):
+            if lens[b]:
+                dec.kv4_append(kv[0][b], kv[1][b], where[b], cache)
+        pools = [cache]
+    dbg, word = _debug()
+    out = torch.full((len(lens), hkv * g, d), 77.0, device="cuda")
+    _run_attention(kind, dec, q, pools, addr, page, window, sinks, dbg, out)
+    assert _flags(word) == 0
+    return dict(kind=kind, dec=dec, q=q, pools=pools, kv=kv, where=where, addr=addr, page=page, window=window,
+                sinks=sinks, lens=lens, out=out, d=d, hkv=hkv, g=g, dtype=dtype)
+
+
+def _check_attention(c):
+    # tensor-core sums may truncate (2^-23); the 4-bit path holds q and the weights in two fp16 parts (2^-22)
+    u = {"window": 2.0 ** -23 if c["dtype"] == "bf16" else 2.0 ** -24, "kv4": 2.0 ** -22}[c["kind"]]
+    d, worst = c["d"], 0.0
+    for b, n in enumerate(c["lens"]):
+        keep = torch.tensor(_seen(n, c["window"], c["sinks"]), dtype=torch.int64, device="cuda")
+        if not len(keep):
+            assert not c["out"][b].any()
+            continue
+        for h in range(c["hkv"]):
+            if c["kind"] == "kv4":
+                k, v = _values64(c["pools"][0][c["where"][b][keep], h], d)
+            else:
+                k, v = (c["kv"][i][b][keep, h].double() for i in range(2))
+            heads = slice(h * c["g"], (h + 1) * c["g"])
+            want, tol = _attention_reference(c["q"][b, heads].double(), k, v, 1 / math.sqrt(d), u)
+            err = (c["out"][b, heads].double() - want).abs()
+            assert (err <= tol).all(), (b, h, float((err / tol).max()))
+            worst = max(worst, float((err / tol).max()))
+    return worst
+
+
+CASES = [  # lens, window, sinks
+    ([1], 1, 0), ([1, 0, 2, 31, 32, 33], 0, 0), ([64, 65, 100, 0], 7, 0), ([300, 5, 40, 260], 33, 4),
+    ([1000, 999], 1, 1), ([129, 700], 128, 500), ([2500], 64, 3), ([4100, 17, 2049], 1000, 36),
+    ([33, 34, 96, 97], 64, 1), ([0, 0], 5, 5), ([200] * 20, 10, 2),
+]
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+@pytest.mark.parametrize("dtype,d,hkv,g,page", [
+    ("bf16", 128, 2, 4, 0), ("bf16", 64, 1, 8, 32), ("f32", 64, 1, 4, 0), ("f32", 128, 3, 1, 96),
+    ("bf16", 128, 1, 7, 64), ("bf16", 64, 4, 3, 0), ("f32", 64, 2, 5, 32), ("f32", 128, 1, 8, 0),
+    ("bf16", 128, 8, 1, 0), ("bf16", 128, 3, 2, 32), ("f32", 64, 1, 6, 0),
+])
+def test_attention(kind, dtype, d, hkv, g, page):
+    """Every case with NaN in all rows that no query may see, and NaN pages and unread table entries around."""
+    for i, (lens, window, sinks) in enumerate(CASES):
+        _check_attention(_attention_case(kind, dtype, d, hkv, g, lens, window, sinks, page, seed=i))
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+@pytest.mark.parametrize("garbage", [math.nan, math.inf, -math.inf])
+def test_masked_keys_do_not_matter(kind, garbage):
+    """Keys of the sequence itself that lie outside the window: any content, the same bits."""
+    for page in (0, 32):
+        c = _attention_case(kind, "bf16", 128, 2, 4, [400, 77], 50, 3, page, seed=5)
+        for b, n in enumerate(c["lens"]):
+            hide = torch.tensor([i for i in range(n) if i not in _seen(n, 50, 3)], device="cuda")
+            for pool in c["pools"]:
+                pool[c["where"][b][hide]] = 0xFF if kind == "kv4" else garbage
+        again = _run_attention(kind, c["dec"], c["q"], c["pools"], c["addr"], page, 50, 3)
+        assert torch.equal(again, c["out"])
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_long_and_many(kind):
+    """A long sequence split over the whole GPU, a batch of unequal ones, more sequences than a CTA has threads."""
+    _check_attention(_attention_case(kind, "bf16", 128, 1, 4, [40000], 0, 0, 0, seed=1))
+    _check_attention(_attention_case(kind, "bf16", 128, 2, 8, [9000, 1, 3000, 0, 12345, 64], 5000, 4, 64, seed=2))
+    _check_attention(_attention_case(kind, "f32", 64, 1, 2, [5000, 9000], 0, 0, 32, seed=3))
+    rng = np.random.default_rng(4)
+    _check_attention(_attention_case(kind, "bf16", 64, 1, 1, rng.integers(0, 50, 1100).tolist(), 20, 2, 32, seed=4))
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_large_logits_and_offsets(kind):
+    """Logits of hundreds (weights that underflow) and keys with a common offset."""
+    _check_attention(_attention_case(kind, "bf16", 128, 2, 4, [3000, 50], 0, 0, 0, seed=6, q_scale=20.0))
+    _check_attention(_attention_case(kind, "f32", 64, 2, 4, [3000, 50], 700, 4, 32, seed=7, q_scale=20.0))
+    _check_attention(_attention_case(kind, "bf16", 128, 2, 4, [2000], 0, 0, 0, seed=8, k_shift=3.0))
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_values_of_any_scale(kind):
+    """Rows whose values span many powers of two, and rows of one value: the tolerance is relative to them."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    for factor in (1e-4, 1.0, 1e3):
+        n, d = 500, 128
+        q = torch.randn((1, 4, d), generator=gen, device="cuda").bfloat16()
+        k = torch.randn((n, 1, d), generator=gen, device="cuda").bfloat16()
+        v = (torch.randn((n, 1, d), generator=gen, device="cuda") * factor
+             * torch.exp2(-torch.randint(0, 6, (n, 1, 1), generator=gen, device="cuda").float())).bfloat16()
+        v[7] = 0
+        v[8] = factor
+        dec = Decoder(1, 4, 1, d, n, n, 256, 1, "bf16")
+        ind = torch.tensor([0, n], device="cuda")
+        if kind == "kv4":
+            cache = dec.kv4_cache()
+            dec.kv4_append(k, v, None, cache)
+            out = dec.kv4(q, cache, ind)
+            kk, vv = _values64(cache[:, 0], d)
+        else:
+            out = dec.window(q, k, v, ind, 0)
+            kk, vv = k[:, 0].double(), v[:, 0].double()
+        want, tol = _attention_reference(q[0].double(), kk, vv, 1 / math.sqrt(d), 2.0 ** -22)
+        assert ((out[0].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_window_of_everything_equals_no_window(kind):
+    c = _attention_case(kind, "bf16", 128, 2, 4, [700, 32, 1], 0, 0, 0, seed=9)
+    for window, sinks in ((700, 0), (10**9, 7), (2**31 - 1, 2**31 - 1), (1, 2**31 - 1), (1, 699)):
+        got = _run_attention(kind, c["dec"], c["q"], c["pools"], c["addr"], 0, window, sinks)
+        assert torch.equal(got, c["out"]) or torch.allclose(got, c["out"], rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_paged_equals_contiguous_and_calls_repeat(kind):
+    """Bit for bit: the cache's layout and the call's timing do not change the result; the workspace's
+    counters are zero again."""
+    a = _attention_case(kind, "bf16", 128, 2, 4, [5000, 300, 0, 31], 2000, 4, 0, seed=10)
+    dec, where = a["dec"], a["where"]
+    page, pages_per = 32, [-(-n // 32) for n in a["lens"]]
+    num = sum(pages_per) + 1
+    pools = [torch.zeros((num * page, *p.shape[1:]), dtype=p.dtype, device="cuda") for p in a["pools"]]
+    table = np.full((4, max(pages_per)), -1, np.int32)
+    ids = np.random.default_rng(0).permutation(num)
+    at = 0
+    for b, n in enumerate(a["lens"]):
+        table[b, :pages_per[b]] = ids[at:at + pages_per[b]]
+        at += pages_per[b]
+        i = np.arange(n)
+        rows = torch.from_numpy(table[b, i // page].astype(np.int64) * page + i % page).cuda()
+        for pool, src in zip(pools, a["pools"]):
+            pool[rows] = src[where[b]]
+    pdec = Decoder(4, 8, 2, 128, num * page, 5000, 256, 1, "bf16")
+    addr = dict(table=torch.from_numpy(table).cuda(), lens=torch.tensor(a["lens"], dtype=torch.int32, device="cuda"))
+    for _ in range(5):
+        assert torch.equal(_run_attention(kind, pdec, a["q"], pools, addr, page, 2000, 4), a["out"])
+        assert torch.equal(_run_attention(kind, dec, a["q"], a["pools"], a["addr"], 0, 2000, 4), a["out"])
+    assert not dec.split_workspace()[:4 * 2 * 4].any()
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_bad_device_data_is_flagged(kind):
+    c = _attention_case(kind, "bf16", 128, 1, 2, [100, 64, 200], 0, 0, 0, seed=12)
+    dbg, word = _debug()
+    ind = c["addr"]["indptr"].clone()
+    ind[1] = 10**12
+    got = _run_attention(kind, c["dec"], c["q"], c["pools"], dict(indptr=ind), 0, 0, 0, dbg)
+    assert _flags(word) == sd.ERR_INDPTR
+    assert not got[:2].any() and torch.equal(got[2], c["out"][2])
+    p = _attention_case(kind, "bf16", 128, 1, 2, [100, 64, 200], 0, 0, 32, seed=12)
+    table = p["addr"]["table"].clone()
+    table[0, 1], table[2, 0] = -1, 10**9  # pages dropped: their keys carry no weight
+    lens = p["addr"]["lens"].clone()
+    lens[1] = -5
+    got = _run_attention(kind, p["dec"], p["q"], p["pools"], dict(table=table, lens=lens), 32, 0, 0, dbg)
+    assert _flags(word) == sd.ERR_INDPTR
+    assert not got[1].any() and torch.isfinite(got).all()
+    keep = {0: [i for i in range(100) if i // 32 != 1], 2: [i for i in range(200) if i // 32 != 0]}
+    for b, rows in keep.items():
+        rows = p["where"][b][torch.tensor(rows, device="cuda")]
+        if kind == "kv4":
+            k, v = _values64(p["pools"][0][rows, 0], 128)
+        else:
+            k, v = (x[rows, 0].double() for x in p["pools"])
+        want, tol = _attention_reference(p["q"][b].double(), k, v, 1 / math.sqrt(128), 2.0 ** -22)
+        assert ((got[b].double() - want).abs() <= tol).all()
+
+
+# ------------------------------------------------------------------------------ 4-bit cache
+
+
+def _quantised(x):
+    """Record parts by the definition, in numpy single precision: codes [..][d / 2], pairs [..][d / 64][2]."""
+    x = x.float().cpu().numpy()
+    d = x.shape[-1]
+    x = np.clip(np.nan_to_num(x, nan=0.0, posinf=65504, neginf=-65504), -65504, 65504).astype(np.float32)
+    g = (np.arange(d) // 8) % (d // 64)
+    codes, pairs = np.zeros(x.shape, np.uint8), np.zeros((*x.shape[:-1], d // 64, 2), np.float16)
+    for i in range(d // 64):
+        r = x[..., g == i]
+        lo = r.min(-1).astype(np.float16)
+        scale = ((r.max(-1) - lo.astype(np.float32)) * np.float32(1.0 / 15.0)).astype(np.float16)
+        s = scale.astype(np.float32)[..., None]
+        with np.errstate(all="ignore"):
+            n = np.rint((r - lo.astype(np.float32)[..., None]) / s)
+        codes[..., g == i] = np.where(s > 0, np.clip(np.nan_to_num(n), 0, 15), 0).astype(np.uint8)
+        pairs[..., i, 0], pairs[..., i, 1] = scale, lo
+    return codes[..., 0::2] | (codes[..., 1::2] << 4), pairs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,hkv,fused", [(1, 1, False), (5, 3, True), (64, 8, True), (1000, 2, False)])
+def test_kv4_append_and_read(dtype, d, T, hkv, fused):
+    dt = DT[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    kv = torch.randn((T, 2 * hkv + 1, d), generator=gen, device="cuda").to(dt)
+    kv[0, 0] = 0.25  # one value: scale 0
+    k, v = kv[:, :hkv], kv[:, hkv:2 * hkv]
+    if not fused:
+        k, v = k.contiguous(), v.contiguous()
+    if T > 4:
+        v[1, 0] *= 1e-6  # fp16 subnormals
+        v[2, 0] *= 3000.0
+    rows = T + 5
+    slots = torch.randperm(rows, generator=gen, device="cuda")[:T].contiguous()
+    if T > 1:
+        slots[T - 1] = -1
+    dec = Decoder(1, hkv, hkv, d, rows, rows, 256, 1, dtype)
+    cache = dec.kv4_cache()
+    cache.fill_(0xAB)
+    dbg, word = _debug()
+    dec.kv4_append(k, v, slots, cache, debug=dbg)
+    kr, vr = dec.kv4_read(cache, slots, debug=dbg)
+    assert _flags(word) == 0
+    live = slots >= 0
+    rec = cache[slots[live]]
+    for x, got, a, b in ((k, kr, 0, d), (v, vr, d // 2, d + d // 16)):
+        codes, pairs = _quantised(x[live])
+        assert np.array_equal(rec[..., a:a + d // 2].cpu().numpy(), codes)
+        assert np.array_equal(rec[..., b:b + d // 16].contiguous().view(torch.float16).cpu().numpy().reshape(pairs.shape), pairs)
+        values = _values64(rec, d)[0 if a == 0 else 1]
+        assert torch.equal(got[live], values.to(dt))  # fp32: base + scale * code is exact to half a step
+        assert not got[~live].any()
+        # half a step of the scale, and the roundings of the minimum (fp16) and of the scale (15 steps of 2^-11)
+        scale = torch.from_numpy(pairs[..., 0].astype(np.float64)).cuda()
+        lo = torch.from_numpy(np.abs(pairs[..., 1]).astype(np.float64)).cuda()
+        g = (torch.arange(d, device="cuda") // 8) % (d // 64)
+        tol = scale[..., g] * (0.5 + 16 * 2.0 ** -11) + lo[..., g] * 2.0 ** -10 + 16 * 2.0 ** -24
+        assert ((values - x[live].double()).abs() <= tol).all()
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[slots[live]] = False
+    assert (cache[rest] == 0xAB).all()
+
+
+def test_kv4_special_values_and_slots():
+    T, d = 6, 64
+    k = torch.randn((T, 1, d), device="cuda")
+    v = torch.randn((T, 1, d), device="cuda")
+    k[0, 0, 5], k[1, 0, 6], v[2, 0, 7], v[3, 0, 0] = math.nan, math.inf, -math.inf, 1e30
+    dec = Decoder(1, 1, 1, d, T, T, 256, 1, "f32")
+    cache = dec.kv4_cache()
+    dbg, word = _debug()
+    dec.kv4_append(k, v, None, cache, debug=dbg)
+    assert _flags(word) == sd.ERR_VALUE
+    for x, a, b in ((k, 0, d), (v, d // 2, d + d // 16)):
+        codes, pairs = _quantised(x)
+        assert np.array_equal(cache[..., a:a + d // 2].cpu().numpy(), codes)
+        assert np.array_equal(cache[..., b:b + d // 16].contiguous().view(torch.float16).cpu().numpy().reshape(pairs.shape), pairs)
+    kr, vr = dec.kv4_read(cache, torch.tensor([T, 2**40, -1, 4], device="cuda"), debug=dbg)
+    assert _flags(word) == sd.ERR_SLOT
+    assert not kr[:3].any() and kr[3].any() and torch.isfinite(vr).all()
+    before = cache.clone()
+    dec.kv4_append(k[:2].contiguous(), v[:2].contiguous(), torch.tensor([T, -7], device="cuda"), cache, debug=dbg)
+    assert _flags(word) == sd.ERR_SLOT and torch.equal(cache, before)
+
+
+# ------------------------------------------------------------------------------ together
+
+
+def _step_state(kind, batch=5, hq=8, hkv=2, d=128, page=32, steps=40):
+    """A small serving loop's buffers: prompts of different lengths, then one token per sequence and step."""
+    num_pages, max_pages = 64, 12
+    dec = Decoder(batch, hq, hkv, d, num_pages * page, max_pages * page, 256, 1, "bf16")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    s = dict(dec=dec, page=page, table=torch.full((batch, max_pages), -1, **i32), lens=torch.zeros(batch, **i32),
+             cs=rope_table(max_pages * page, d), kw=torch.ones(d, device="cuda").bfloat16() * 1.25, num_pages=num_pages,
+             free=torch.from_numpy(np.random.default_rng(0).permutation(num_pages).astype(np.int32)).cuda())
+    if kind == "kv4":
+        s["cache"] = dec.kv4_cache()
+    rows = [torch.full((num_pages * page, hkv, d), math.nan, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    s["k"], s["v"] = rows
+    return s
+
+
+def _step(kind, s, new, qkv, max_tokens, window, sinks, lens_out, slots, pos, counts):
+    dec, (hq, hkv) = s["dec"], (s["dec"].problem.num_q_heads, s["dec"].problem.num_kv_heads)
+    dec.page_plan(s["lens"], new, s["table"], s["free"], s["page"], slots, pos, lens_out, counts)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    if kind == "kv4":  # rotate into a row per token, then store 4 bits
+        kr, vr = torch.empty_like(k, memory_format=torch.contiguous_format), v
+        tok = Decoder(1, hq, hkv, dec.problem.head_dim, max_tokens, max_tokens, 256, 1, "bf16")
+        qr = tok.norm_rope(q, k, None, pos, None, s["cs"], kr, None, s["kw"], s["kw"])
+        dec.kv4_append(kr, vr, slots, s["cache"])
+    else:
+        qr = dec.norm_rope(q, k, v, pos, slots, s["cs"], s["k"], s["v"], s["kw"], s["kw"])
+    return qr
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_a_serving_loop(kind):
+    """Prompts are placed, then tokens are decoded one by one: the loop's outputs against the whole history
+    held densely in 64 bits (the 4-bit cache's own values for kv4)."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    s = _step_state(kind)
+    dec, d, hq, hkv, B = s["dec"], 128, 8, 2, 5
+    prompts = [40, 1, 0, 97, 64]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    free_host = s["free"].cpu().numpy()
+    hist = [[] for _ in range(B)]  # (rotated key, value) rows in 64 bits
+    window, sinks = 50, 3
+    for step in range(6):
+        new = prompts if step == 0 else [1] * B
+        max_tokens = sum(new) + 3
+        qkv = torch.randn((max_tokens, hq + 2 * hkv, d), generator=gen, device="cuda").bfloat16()
+        slots, pos = torch.empty(max_tokens, dtype=torch.int64, device="cuda"), torch.empty(max_tokens, **i32)
+        lens_out, counts = torch.empty(B, **i32), torch.empty(2, **i32)
+        qr = _step(kind, s, torch.tensor(new, **i32), qkv, max_tokens, window, sinks, lens_out, slots, pos, counts)
+        s["lens"] = lens_out
+        taken = int(counts[0])
+        free_host = free_host[taken:]
+        s["free"] = torch.from_numpy(free_host.copy()).cuda()
+        t = 0
+        for b in range(B):
+            for i in range(new[b]):
+                hist[b].append(int(slots[t]))
+                assert int(pos[t]) == len(hist[b]) - 1
+                t += 1
+        assert (slots[t:] == -1).all()
+        if step == 0:
+            continue
+        out = (dec.kv4_paged(qr[:B].contiguous(), s["cache"], s["table"], s["lens"], s["page"], window, sinks) if kind == "kv4"
+               else dec.window_paged(qr[:B].contiguous(), s["k"], s["v"], s["table"], s["lens"], s["page"], window, sinks))
+        for b in range(B):
+            keep = torch.tensor(_seen(len(hist[b]), window, sinks), device="cuda")
+            rows = torch.tensor(hist[b], device="cuda")[keep]
+            for h in range(hkv):
+                if kind == "kv4":
+                    k, v = _values64(s["cache"][rows, h], d)
+                else:
+                    k, v = s["k"][rows, h].double(), s["v"][rows, h].double()
+                heads = slice(4 * h, 4 * h + 4)
+                want, tol = _attention_reference(qr[b, heads].double(), k, v, 1 / math.sqrt(d), 2.0 ** -22)
+                assert ((out[b, heads].double() - want).abs() <= tol).all()
+    assert [len(x) for x in hist] == s["lens"].tolist()
+    assert len({r for x in hist for r in x}) == sum(len(x) for x in hist)  # no row twice
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_captured_step_replays_on_new_inputs(kind):
+    """Plan, rotation, store and attention in one CUDA graph; replays on other lengths, keys and queries equal
+    eager calls bit for bit."""
+    B, hq, hkv, d, page = 4, 8, 2, 128, 32
+    s = _step_state(kind, batch=B)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    new = torch.ones(B, **i32)
+    qkv = torch.zeros((B, hq + 2 * hkv, d), device="cuda", dtype=torch.bfloat16)
+    slots, pos = torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty(B, **i32)
+    lens_out, counts = torch.empty(B, **i32), torch.empty(2, **i32)
+    out = torch.empty((B, hq, d), device="cuda")
+    s["k"].normal_(), s["v"].normal_()
+    if kind == "kv4":
+        allrows = torch.arange(s["num_pages"] * page, device="cuda")
+        s["dec"].kv4_append(s["k"], s["v"], allrows, s["cache"])
+    dec = s["dec"]
+
+    def step():
+        qr = _step(kind, s, new, qkv, B, 100, 4, lens_out, slots, pos, counts)
+        if kind == "kv4":
+            dec.kv4_paged(qr, s["cache"], s["table"], lens_out, page, 100, 4, out=out)
+        else:
+            dec.window_paged(qr, s["k"], s["v"], s["table"], lens_out, page, 100, 4, out=out)
+
+    def load(i):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        qkv.copy_(torch.randn(qkv.shape, generator=g, device="cuda"))
+        lens = [(37 * i + 61 * b) % 300 for b in range(B)]
+        s["lens"].copy_(torch.tensor(lens, **i32))
+        ids = np.random.default_rng(i).permutation(s["num_pages"]).astype(np.int32)
+        table, at = np.full(tuple(s["table"].shape), -1, np.int32), 0
+        for b, n in enumerate(lens):
+            have = -(-n // page)
+            table[b, :have] = ids[at:at + have]
+            at += have
+        s["table"].copy_(torch.from_numpy(table))
+        s["free"][:len(ids) - at].copy_(torch.from_numpy(ids[at:]))
+
+    load(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (1, 2, 3):
+        load(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (out, slots, pos, lens_out, s["table"])]
+        load(i)
+        step()
+        for a, b in zip(got, (out, slots, pos, lens_out, s["table"])):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_two_streams_with_a_workspace_each(kind):
+    cases = [_attention_case(kind, "bf16", 128, 2, 4, [6000, 10, 3000], 0, 0, 0, seed=30 + i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                outs.append((c, _run_attention(kind, c["dec"], c["q"], c["pools"], c["addr"], 0, 0, 0)))
+    torch.cuda.synchronize()
+    for c, got in outs:
+        assert torch.equal(got, c["out"])
+
+
+def test_rows_beyond_32_bit_offsets():
+    """A cache of more than 2^32 bytes (and 2^31 elements of a 4-bit one): the last rows are found."""
+    hkv, d = 8, 128
+    rows = (1 << 32) // (hkv * 144) + 64
+    dec = Decoder(1, hkv, hkv, d, rows, 64, 256, 1, "bf16")
+    cache = torch.empty((rows, hkv, 144), dtype=torch.uint8, device="cuda")
+    k, v, q = (torch.randn((64, hkv, d), device="cuda").bfloat16() for _ in range(3))
+    slots = torch.arange(rows - 64, rows, device="cuda")
+    dec.kv4_append(k, v, slots, cache)
+    ind = torch.tensor([rows - 64, rows], device="cuda")
+    out = dec.kv4(q[:1].contiguous(), cache, ind)
+    kc = torch.empty((rows, hkv, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    pos = torch.zeros(64, dtype=torch.int32, device="cuda")
+    dec.norm_rope(None, k, v, pos, slots, rope_table(4, d), kc, vc)
+    assert torch.equal(kc[slots], k) and torch.equal(vc[slots], v)
+    win = dec.window(q[:1].contiguous(), kc, vc, ind, 0)
+    for h in range(hkv):
+        k4, v4 = _values64(cache[slots, h], d)
+        for got, (kk, vv) in ((out, (k4, v4)), (win, (k[:, h].double(), v[:, h].double()))):
+            want, tol = _attention_reference(q[:1, h].double(), kk, vv, 1 / math.sqrt(d), 2.0 ** -22)
+            assert ((got[0, h].double() - want[0]).abs() <= tol[0]).all()
