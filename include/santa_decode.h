@@ -510,11 +510,13 @@ typedef struct {
  * and v are page pools and kv_indptr is unused, as in santa_decode_prop_paged.  What
  * keys outside the window hold (infinities and NaN included) does not matter.  An
  * empty sequence gives zeros.  Results do not depend on timing: equal calls give
- * equal bits.
+ * equal bits.  What the visible keys and values hold must be finite (else a head's
+ * output may be NaN where a plain sum would be infinite).
  * Workspace: santa_split_workspace_size, prepared once by santa_split_workspace_init;
  * every call leaves it ready for the next, of santa_decode_window or santa_decode_kv4
  * on the same problem, and calls that may overlap (two graphs, two streams) need one
- * each.
+ * each.  After SANTA_ERR_TIMEOUT the call's outputs are not valid and the workspace
+ * must be prepared again.
  */
 int santa_decode_window(const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
                         const void *k, const void *v, const long long *kv_indptr, float *out, void *workspace,

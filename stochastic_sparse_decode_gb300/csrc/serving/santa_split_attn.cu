@@ -123,9 +123,6 @@ cudaError_t launch(const SplitParams &sp, cudaStream_t stream, const Timing &tm)
 
 }  // namespace
 
-cudaError_t launch_window(const SplitParams &sp, int dtype, cudaStream_t stream, const Timing &tm) {
-    return dtype == SANTA_BF16 ? launch<uint16_t, uint16_t>(sp, stream, tm) : launch<float, float>(sp, stream, tm);
-}
 cudaError_t launch_kv4(const SplitParams &sp, int dtype, cudaStream_t stream, const Timing &tm) {
     return dtype == SANTA_BF16 ? launch<Kv4Elem, uint16_t>(sp, stream, tm) : launch<Kv4Elem, float>(sp, stream, tm);
 }

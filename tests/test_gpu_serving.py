@@ -518,7 +518,10 @@ def test_bad_device_data_is_flagged(kind):
     ind[1] = 10**12
     got = _run_attention(kind, c["dec"], c["q"], c["pools"], dict(indptr=ind), 0, 0, 0, dbg)
     assert _flags(word) == sd.ERR_INDPTR
-    assert not got[:2].any() and torch.equal(got[2], c["out"][2])
+    assert not got[:2].any()
+    # where a head is cut depends on the other sequences' lengths: equal to rounding, not to the bit
+    one = dict(c, out=got, lens=[0, 0, 200])
+    _check_attention(one)
     p = _attention_case(kind, "bf16", 128, 1, 2, [100, 64, 200], 0, 0, 32, seed=12)
     table = p["addr"]["table"].clone()
     table[0, 1], table[2, 0] = -1, 10**9  # pages dropped: their keys carry no weight
