@@ -2,23 +2,27 @@
 //
 // A key row stands for k_i = m_g + s_g n_i (codes n_i in 0 .. 15; scale s_g and minimum m_g
 // of element i's group g), a value row likewise, so
-//   q . k_j     = sum_g s_jg (q_g . n_jg) + m_jg sum(q_g)
-//   sum_j e_j v_j = sum_j (e_j s_jg) n_j  + sum_j e_j m_jg          (group by group),
+//   q . k_j       = sum_g s_jg (q_g . n_jg) + m_jg sum(q_g)
+//   sum_j e_j v_j = sum_j (e_j s_jg) n_j    + sum_j e_j m_jg          (group by group),
 // and both large products run on the tensor cores (fp16 mma m16n8k16) on the codes as
 // they lie in memory.  A code needs no conversion: masked out of its word it is, as an fp16
 // bit pattern, the subnormal n 2^-24 (low nibble of a byte) or n 2^-20 (high nibble), which
 // the tensor cores multiply exactly; the powers of two go into q and the final factor.
-// One 32-bit word of K gives a lane the A fragments of two products (4 ands, 1 shift); a
-// word of V, paired with the next key's by byte permutes, those of four (2 permutes, 8
-// ands, 2 shifts), so nothing is staged through shared memory: codes go from global
-// memory to registers, the next block's while the current one is computed.
+// Queries and weights are the A operand (rows = heads), codes the B operand, so the logits
+// come out in the layout in which the weights go in, and a lane deals with one head.  A word
+// of K's codes is the B operand of two products (4 ands, 1 shift); two keys' words of V,
+// paired by byte permutes, those of eight (2 permutes, 8 ands, 2 shifts).  Nothing is staged
+// through shared memory but the rows' scales and minima, converted once by the lane that
+// has the key; codes go from global memory to registers, the next block's while the current
+// one is computed.
 //
 // Precision: q is scaled by a power of two per head to fit fp16 (a bf16 q is exact so; an
-// fp32 q is taken in two parts, 22 bits), the weights e_j s_jg in two parts (22 bits) under
-// a running power of two that keeps the largest scale of the row's values in range;
-// everything else is fp32.  The online softmax and the sharing out of the keys are those
-// of the windowed kernel (santa_split.cuh): each block's sums start from zero and join O
-// by an fp32 fma.
+// fp32 q is taken in two parts, 22 bits, the second in the A operand's rows 8 .. 15); the
+// weights e_j s_jg likewise in two parts, rows 0 .. 7 and 8 .. 15 of one product, under a
+// running power of two that keeps the largest scale of the row's values in range.
+// Everything else is fp32.  The online softmax and the sharing out of the keys are those of
+// the windowed kernel (santa_split.cuh): each block's sums start from zero and join O by an
+// fp32 fma.
 #include <cuda_fp16.h>
 
 #include "santa_split.cuh"
@@ -27,19 +31,24 @@ namespace santa {
 
 namespace {
 
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d = A B (+ d): A's rows 0 .. 7 are (a0, a2), rows 8 .. 15 (a1, a3).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// (x, y) as an fp16 pair, and what the rounding left.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (x, y) as an fp16 pair; x and y become what the rounding left.
 __device__ __forceinline__ uint32_t half_pair(float &x, float &y) {
     const __half2 h = __floats2half2_rn(x, y);
     x -= __low2float(h);
@@ -58,350 +67,396 @@ __device__ __forceinline__ int exponent(float x) {
 
 constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
-template <int D, int GT>
+template <int D, typename Q, int GT>
 struct Kv4Geom {
     static constexpr int kWarps = 12;
-    static constexpr size_t kPieces = size_t(kWarps) * 2 * GT * D * 4;  // first and last pieces
-    static constexpr size_t kTotal = kPieces + sizeof(SplitShared<kWarps>);
-    static_assert(size_t(kSplitCtaBound) * GT * 4 + size_t(kWarps) * 32 * 16 <= kPieces, "room to join");
+    static constexpr int kG = D / 64;
+    static constexpr int kQ = sizeof(Q) == 2 ? 1 : 2;       // fp16 parts of q
+    static constexpr int kParBytes = kBlock * kG * 16;      // a block's (scale, minimum) of K and of V in fp32
+    static constexpr int kQBytes = 32 * (D / 32) * 16 * kQ; // a warp's A operand of q
+    // shared memory: first and last pieces [kWarps][2][GT][D], q and parameters per warp, shared state
+    static constexpr size_t kQOff = size_t(kWarps) * 2 * GT * D * 4;
+    static constexpr size_t kParOff = kQOff + size_t(kWarps) * kQBytes;
+    static constexpr size_t kShared = kParOff + size_t(kWarps) * kParBytes;
+    static constexpr size_t kTotal = kShared + sizeof(SplitShared<kWarps>);
+    static_assert(size_t(kSplitCtaBound) * kMaxGroup * 4 + size_t(kWarps) * 32 * 16 <= kParOff, "room to join");
     static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
-// What a lane (g = lane / 4, t = lane % 4) loads of a block of 32 records.
-template <int D>
-struct Block4 {
-    static constexpr int kW = D / 32;  // words of K's codes per key and lane; V: kW / 2
-    static constexpr int kG = D / 64;
-    uint32_t k[4][kW];          // keys 8 o + g: words kW t ..
-    uint32_t v[4][2][kW / 2];   // keys 8 o + 2t + i: words kW / 2 g ..
-    uint32_t par[2 * kG];       // key `lane`: (scale, minimum) of K's groups, then V's
-};
-
 template <int D, typename Q, int GT, bool kPaged>
-__global__ void __launch_bounds__(Kv4Geom<D, GT>::kWarps * 32, 1) kv4_kernel(const __grid_constant__ SplitParams sp) {
-    using Geom = Kv4Geom<D, GT>;
-    using Blk = Block4<D>;
-    constexpr int NW = Geom::kWarps, kW = Blk::kW, kG = Blk::kG, kTiles = D / 16;
-    constexpr int kQ = sizeof(Q) == 2 ? 1 : 2;  // fp16 parts of q
+__global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(const __grid_constant__ SplitParams sp) {
+    using Geom = Kv4Geom<D, Q, GT>;
+    constexpr int NW = Geom::kWarps, kG = Geom::kG, kQ = Geom::kQ;
+    constexpr int kW = D / 32;   // words of K's codes per key and lane; V: kW / 2
+    constexpr int kTiles = D / 8;
     constexpr int kRec = kv4_record(D);
     const Params &p = sp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = p.G;
     extern __shared__ __align__(16) unsigned char smem[];
     float *pieces = reinterpret_cast<float *>(smem);  // [warp][first, last][GT][D]
-    SplitShared<NW> &sh = *reinterpret_cast<SplitShared<NW> *>(smem + Geom::kPieces);
+    uint4 *qa = reinterpret_cast<uint4 *>(smem + Geom::kQOff + warp * Geom::kQBytes);       // [word][part][lane]
+    float4 *par = reinterpret_cast<float4 *>(smem + Geom::kParOff + warp * Geom::kParBytes);  // see stage
+    SplitShared<NW> &sh = *reinterpret_cast<SplitShared<NW> *>(smem + Geom::kShared);
     if (lane < 2) sh.u0[2 * warp + lane] = -1;
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
 
     Walk w;
-    const bool any = plan_walk<NW, kPaged>(sp, sh, w);
-    if ((int)blockIdx.x >= w.ctas) return;
+    const int any = plan_walk<NW, kPaged>(sp, sh, w);
+    if (any < 0) return;
 
     const uint32_t step = uint32_t(p.Hkv) * kRec;  // bytes from a key's record to the next key's
-    Blk blk;
-    // Record of the first key of block n of head h, null for a bad page (its keys are dropped).
-    auto block_at = [&](const Head &h, int key0) -> const unsigned char * {
-        const long long row = key_row<kPaged>(p, h.b, h.start, key0);
-        return row < 0 ? nullptr : sp.kv4 + ((size_t)row * p.Hkv + h.kvh) * kRec;
+    // a block's codes: K of keys 8 o + g (words kW t ..), V of keys 8 o + 2t + i (words kW / 2 g ..),
+    // and key `lane`'s pairs (scale, minimum): K's groups, then V's
+    uint32_t kc[4][kW], vc[4][2][kW / 2], pc[2 * kG];
+    // which keys of the walk's block the query sees, a bit each
+    auto seen_bits = [&]() {
+        const int key = w.key0 + lane;
+        const Visible &v = w.head.vis;
+        return __ballot_sync(kFull, w.row >= 0 && key < v.L && (key < v.s || key >= v.lo));
     };
-    // which keys of the block at key0 the query sees, a bit each
-    auto seen_bits = [&](const Head &h, int key0, const unsigned char *rec) {
-        const int key = key0 + lane;
-        return __ballot_sync(kFull, rec && key < h.vis.L && (key < h.vis.s || key >= h.vis.lo));
-    };
+    auto record = [&]() { return sp.kv4 + ((size_t)(w.row < 0 ? 0 : w.row) * p.Hkv + w.head.kvh) * kRec; };
     auto load_k = [&](const unsigned char *rec, unsigned seen) {
+        const unsigned char *src = rec + g * step + t * (kW * 4);
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
-            const int r = 8 * o + g;
-            const unsigned char *src = rec + r * step + t * (kW * 4);
+            const bool in = seen >> (8 * o + g) & 1;
             if constexpr (kW == 4) {
-                const uint4 x = seen >> r & 1 ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-                blk.k[o][0] = x.x, blk.k[o][1] = x.y, blk.k[o][2] = x.z, blk.k[o][3] = x.w;
+                const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+                kc[o][0] = x.x, kc[o][1] = x.y, kc[o][2] = x.z, kc[o][3] = x.w;
             } else {
-                const uint2 x = seen >> r & 1 ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
-                blk.k[o][0] = x.x, blk.k[o][1] = x.y;
+                const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
+                kc[o][0] = x.x, kc[o][1] = x.y;
             }
+            src += 8 * step;
         }
     };
     auto load_v = [&](const unsigned char *rec, unsigned seen) {
+        const unsigned char *src = rec + 2 * t * step + D / 2 + g * (kW * 2);
 #pragma unroll
-        for (int o = 0; o < 4; ++o)
+        for (int o = 0; o < 4; ++o) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = 8 * o + 2 * t + i;
-                const unsigned char *src = rec + r * step + D / 2 + g * (kW * 2);
+                const bool in = seen >> (8 * o + 2 * t + i) & 1;
+                const unsigned char *at = src + i * step;
                 if constexpr (kW == 4) {
-                    const uint2 x = seen >> r & 1 ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
-                    blk.v[o][i][0] = x.x, blk.v[o][i][1] = x.y;
+                    const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(at)) : make_uint2(0, 0);
+                    vc[o][i][0] = x.x, vc[o][i][1] = x.y;
                 } else {
-                    blk.v[o][i][0] = seen >> r & 1 ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
+                    vc[o][i][0] = in ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
                 }
             }
+            src += 8 * step;
+        }
     };
     auto load_par = [&](const unsigned char *rec, unsigned seen) {
         const unsigned char *src = rec + lane * step + D;
+        const bool in = seen >> lane & 1;
         if constexpr (kG == 2) {
-            const uint4 x = seen >> lane & 1 ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-            blk.par[0] = x.x, blk.par[1] = x.y, blk.par[2] = x.z, blk.par[3] = x.w;
+            const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+            pc[0] = x.x, pc[1] = x.y, pc[2] = x.z, pc[3] = x.w;
         } else {
-            const uint2 x = seen >> lane & 1 ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
-            blk.par[0] = x.x, blk.par[1] = x.y;
+            const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
+            pc[0] = x.x, pc[1] = x.y;
         }
     };
 
-    // State of heads 2t, 2t + 1: M, the lane's own keys' share of Z and of the sums of
-    // e_j m_jg, and O^T: tile (word i of the lane's V words, q) holds elements 2q (Ot[..][j])
-    // and 2q + 1 (Ot[..][2 + j]) of word (kW / 2) g + i, times fscale 2^-24 and 2^-20.
-    float M[2], Z[2], base[kG][2], Ot[kTiles][4], fscale;
+    // State of head g: M, the shares of the lane's own keys of Z and of the sums e_j m_jg, and
+    // O: tile n (a nibble of the lane's V words) holds columns 2t, 2t + 1, that is element n of
+    // words kW / 2 (2t) .. and kW / 2 (2t + 1) .., times fscale 2^-24 (n even) or 2^-20.
+    float M, Z, base[kG], O[kTiles][2], fscale;
     auto reset = [&]() {
-        M[0] = M[1] = -INFINITY;
-        Z[0] = Z[1] = 0.f;
+        M = -INFINITY;
+        Z = 0.f;
         fscale = pow2(60);  // larger than any block allows
 #pragma unroll
-        for (int i = 0; i < kG; ++i) base[i][0] = base[i][1] = 0.f;
+        for (int i = 0; i < kG; ++i) base[i] = 0.f;
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) Ot[m][0] = Ot[m][1] = Ot[m][2] = Ot[m][3] = 0.f;
+        for (int n = 0; n < kTiles; ++n) O[n][0] = O[n][1] = 0.f;
     };
-    auto close = [&](const Head &head, bool final, int slot) {
+    auto close = [&](const Owner &head, bool final, int slot) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int x = 1; x < 4; x <<= 1) {
+            Z += __shfl_xor_sync(kFull, Z, x);
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                Z[j] += __shfl_xor_sync(kFull, Z[j], x);
+            for (int i = 0; i < kG; ++i) base[i] += __shfl_xor_sync(kFull, base[i], x);
+        }
+        if (g < G) {
+            float *dst = final ? p.out + (size_t(head.b) * p.Hq + head.kvh * G + g) * D
+                               : pieces + (size_t(slot) * GT + g) * D;
+            const float inv = !final ? 1.f : Z == 0.f ? 0.f : 1.f / Z;
+            const float f[2] = {16777216.f / fscale, 1048576.f / fscale};  // powers of two
 #pragma unroll
-                for (int i = 0; i < kG; ++i) base[i][j] += __shfl_xor_sync(kFull, base[i][j], x);
-            }
-        const float f = 1.f / fscale;  // a power of two
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int h = 2 * t + j;
-            if (h < G) {
-                float *dst = final ? p.out + (size_t(head.b) * p.Hq + head.kvh * G + h) * D
-                                   : pieces + (size_t(slot) * GT + h) * D;
-                const float inv = !final ? 1.f : Z[j] == 0.f ? 0.f : 1.f / Z[j];
-#pragma unroll
-                for (int m = 0; m < kTiles; ++m) {
-                    const int i = m / 4, at = 8 * (kW / 2 * g + i) + 2 * (m % 4);
-                    *reinterpret_cast<float2 *>(dst + at) =
-                        make_float2(fmaf(Ot[m][j], f * 16777216.f, base[i % kG][j]) * inv,
-                                    fmaf(Ot[m][2 + j], f * 1048576.f, base[i % kG][j]) * inv);
+                for (int n = 0; n < kTiles; n += 4) {
+                    float4 o;
+                    const float b = base[n / 8 % kG];
+                    o.x = fmaf(O[n][c], f[0], b) * inv;
+                    o.y = fmaf(O[n + 1][c], f[1], b) * inv;
+                    o.z = fmaf(O[n + 2][c], f[0], b) * inv;
+                    o.w = fmaf(O[n + 3][c], f[1], b) * inv;
+                    *reinterpret_cast<float4 *>(dst + (2 * t + c) * kTiles + n) = o;
                 }
-                if (!final && g == 0) {
-                    sh.M[slot][h] = M[j];
-                    sh.Z[slot][h] = Z[j];
-                }
+            if (!final && t == 0) {
+                sh.M[slot][g] = M;
+                sh.Z[slot][g] = Z;
             }
         }
         if (!final && lane == 0) note_piece(sh, slot, head);
     };
 
-    if (any) {
-        Head head = w.head;  // of the block being computed; w runs one block ahead
-        const unsigned char *rec = block_at(head, head.first_key(w.n));
-        unsigned seen = seen_bits(head, head.first_key(w.n), rec);
-        load_k(rec, seen);
-        load_par(rec, seen);
-        load_v(rec, seen);
-        const long long x_first = w.x;
-        uint32_t qf[kQ][kW][2][2];  // [part][word][step]: elements (0, 4), (1, 5) / 16, then (2, 6), (3, 7) / 16
-        float qsum[kG][2], kq[2];   // of heads 2t, 2t + 1: sum(q_g), and the factor of the products; base 2
+    if (any > 0) {
+        Owner head(w);  // of the block being computed; w runs one block ahead
+        unsigned seen = seen_bits();
+        {
+            const unsigned char *rec = record();
+            load_par(rec, seen);
+            load_k(rec, seen);
+            load_v(rec, seen);
+        }
+        float qsum[kG], kq = 0.f;  // of head g: sum(q_g) and the logits' factor: x = kq y, base 2
         bool fresh = true;
         reset();
         for (bool more = true; more;) {
+            const bool last = w.n + 1 == head.nb;  // the block is its head's last
             more = next_unit<kPaged>(sp, w);
             const bool same = more && w.head.u0 == head.u0;
             const unsigned char *next = nullptr;
             unsigned next_seen = 0;
             if (more) {
-                next = block_at(w.head, w.head.first_key(w.n));
-                next_seen = seen_bits(w.head, w.head.first_key(w.n), next);
+                next = record();
+                next_seen = seen_bits();
             }
             if (fresh) {
                 fresh = false;
-                // this lane's kW words (8 elements each) of head g
+                // q as the A operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
+                // words kW t + u, the latter / 16 because their codes are high nibbles
                 const Q *qh = static_cast<const Q *>(p.q) + (size_t(head.b) * p.Hq + head.kvh * G + min(g, G - 1)) * D +
                               t * kW * 8;
-                float x[kW][8], mx = 0.f, sum[kG];
+                float x[kW][8], mx = 0.f;
 #pragma unroll
-                for (int i = 0; i < kG; ++i) sum[i] = 0.f;
+                for (int i = 0; i < kG; ++i) qsum[i] = 0.f;
 #pragma unroll
-                for (int u = 0; u < kW; ++u)
+                for (int u = 0; u < kW; ++u) {
+                    constexpr int kVec = 8 * sizeof(Q) / 16;
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) {
+                        float2 pr[Vec16<Q>::kPairs];
+                        Vec16<Q>::unpack(__ldg(reinterpret_cast<const uint4 *>(qh + 8 * u) + i), pr);
+#pragma unroll
+                        for (int j = 0; j < Vec16<Q>::kPairs; ++j) {
+                            x[u][2 * (i * Vec16<Q>::kPairs + j)] = pr[j].x;
+                            x[u][2 * (i * Vec16<Q>::kPairs + j) + 1] = pr[j].y;
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        x[u][i] = g < G ? to_float<Q>(__ldg(qh + 8 * u + i)) : 0.f;
+                        if (g >= G) x[u][i] = 0.f;
                         mx = fmaxf(mx, fabsf(x[u][i]));
-                        sum[u % kG] += x[u][i];
+                        qsum[u % kG] += x[u][i];
                     }
+                }
 #pragma unroll
                 for (int s = 1; s < 4; s <<= 1) {
                     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, s));
 #pragma unroll
-                    for (int i = 0; i < kG; ++i) sum[i] += __shfl_xor_sync(kFull, sum[i], s);
+                    for (int i = 0; i < kG; ++i) qsum[i] += __shfl_xor_sync(kFull, qsum[i], s);
                 }
                 const int e = exponent(mx);
-                const float f = pow2(14 - e);
+                const float f = pow2(14 - e), fh = f * 0.0625f;
+                __syncwarp();
 #pragma unroll
-                for (int u = 0; u < kW; ++u)
+                for (int u = 0; u < kW; ++u) {
+                    float a[8];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * (i & 1 ? fh : f);
 #pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            float a = x[u][2 * s + hi] * f, b = x[u][2 * s + hi + 4] * f;
-                            if (hi) {
-                                a *= 0.0625f;
-                                b *= 0.0625f;
-                            }
-#pragma unroll
-                            for (int i = 0; i < kQ; ++i) qf[i][u][s][hi] = half_pair(a, b);
-                        }
-                const float scale2 = p.scale * 1.4426950408889634f;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int src = 4 * (2 * t + j);
-                    kq[j] = pow2(__shfl_sync(kFull, e, src) + 10) * scale2;  // 2^24 2^(e - 14)
-#pragma unroll
-                    for (int i = 0; i < kG; ++i) qsum[i][j] = __shfl_sync(kFull, sum[i], src) * scale2;
+                    for (int part = 0; part < kQ; ++part)
+                        qa[(u * kQ + part) * 32 + lane] = make_uint4(half_pair(a[0], a[4]), half_pair(a[1], a[5]),
+                                                                     half_pair(a[2], a[6]), half_pair(a[3], a[7]));
                 }
+                // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)): products' units
+                kq = pow2(e + 10) * p.scale * 1.4426950408889634f;
+                const float toy = pow2(-10 - e);
+#pragma unroll
+                for (int i = 0; i < kG; ++i) qsum[i] *= toy;
+                __syncwarp();
             }
 
-            // ---- q . n of the block, group by group: c[mt][group], keys 16 mt + g and + 8
-            float c[2][kG][4];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-                for (int i = 0; i < kG; ++i) c[mt][i][0] = c[mt][i][1] = c[mt][i][2] = c[mt][i][3] = 0.f;
-#pragma unroll
-                for (int u = 0; u < kW; ++u)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint32_t a = blk.k[2 * mt][u] >> (8 * s), b = blk.k[2 * mt + 1][u] >> (8 * s);
-                        const uint32_t frag[4] = {a & kLo, b & kLo, a & kHi, b & kHi};
-#pragma unroll
-                        for (int i = kQ - 1; i >= 0; --i)
-                            mma_f16_16816(c[mt][u % kG], frag, qf[i][u][s][0], qf[i][u][s][1]);
-                    }
-            }
-            if (more) load_k(next, next_seen);
-
-            // ---- online softmax; the weights times the values' scales, as B fragments
-            uint32_t pf[kG][2][4];  // [group][part][octet]
-            float sc[2];
+            // ---- key `lane`'s scales and minima, in fp32, V's scales times the running power of two
+            float lower = 1.f;
             {
-                float e[2][4];
-#pragma unroll
-                for (int o = 0; o < 4; ++o) {
-                    const int r = 8 * o + g;
-                    float y[2] = {0.f, 0.f}, z[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < kG; ++i) {
-                        const float2 sm = half_values(__shfl_sync(kFull, blk.par[i], r));
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            y[j] = fmaf(sm.x, c[o >> 1][i][(o & 1) * 2 + j], y[j]);
-                            z[j] = fmaf(sm.y, qsum[i][j], z[j]);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) e[j][o] = seen >> r & 1 ? fmaf(y[j], kq[j], z[j]) : -INFINITY;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float m = fmaxf(fmaxf(e[j][0], e[j][1]), fmaxf(e[j][2], e[j][3]));
-#pragma unroll
-                    for (int s = 4; s < 32; s <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
-                    m = fmaxf(M[j], m);
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    sc[j] = ex2(M[j] - ref);
-                    M[j] = m;
-                    float z = 0.f;
-#pragma unroll
-                    for (int o = 0; o < 4; ++o) {
-                        e[j][o] = ex2(e[j][o] - ref);
-                        z += e[j][o];
-                    }
-                    Z[j] = fmaf(Z[j], sc[j], z);
-#pragma unroll
-                    for (int i = 0; i < kG; ++i) base[i][j] *= sc[j];
-                }
-                // the largest scale of the block's values decides the power of two
+                float2 sm[2 * kG];
                 float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < kG; ++i) top = fmaxf(top, fabsf(half_values(blk.par[kG + i]).x));
+                for (int i = 0; i < 2 * kG; ++i) sm[i] = half_values(pc[i]);
+#pragma unroll
+                for (int i = 0; i < kG; ++i) top = fmaxf(top, fabsf(sm[kG + i].x));
                 top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(top)));
                 if (top * fscale >= 32768.f) {
-                    const float lower = pow2(14 - exponent(top)), ratio = lower / fscale;
-                    sc[0] *= ratio;
-                    sc[1] *= ratio;
-                    fscale = lower;
+                    const float f = pow2(14 - exponent(top));
+                    lower = f / fscale;
+                    fscale = f;
                 }
+                if (more) load_par(next, next_seen);
+                // [key]: K's (s, m) per group, then V's; slot rotated by the key's pair against bank conflicts
+#pragma unroll
+                for (int i = 0; i < kG; ++i) {
+                    if constexpr (kG == 2) {
+                        const float2 a = sm[2 * i], b = sm[2 * i + 1];
+                        par[lane * 2 + (i ^ (lane >> 2 & 1))] = i == 0 ? make_float4(a.x, a.y, b.x, b.y)
+                                                                      : make_float4(a.x * fscale, a.y, b.x * fscale, b.y);
+                    } else {
+                        par[lane] = make_float4(sm[0].x, sm[0].y, sm[1].x * fscale, sm[1].y);
+                    }
+                }
+                __syncwarp();
+            }
+            // (scale, minimum) per group of K (which = 0) or V (1) of key r
+            auto params = [&](int which, int r) -> float4 {
+                if constexpr (kG == 2) {
+                    return par[r * 2 + (which ^ (r >> 2 & 1))];
+                } else {
+                    const float2 x = reinterpret_cast<const float2 *>(par + r)[which];
+                    return make_float4(x.x, x.y, 0.f, 0.f);
+                }
+            };
+
+            // ---- logits of head g and keys 8 o + 2t + i
+            float y[4][2];
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+                float c[kG][4];
+#pragma unroll
+                for (int u = 0; u < kW; ++u) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t wd = kc[o][u] >> (8 * s), b0 = wd & kLo, b1 = wd & kHi;
+                        const uint4 qh = qa[(u * kQ) * 32 + lane];
+                        uint32_t a1 = 0, a3 = 0;
+                        if constexpr (kQ == 2) {
+                            const uint4 ql = qa[(u * kQ + 1) * 32 + lane];
+                            a1 = s ? ql.z : ql.x;
+                            a3 = s ? ql.w : ql.y;
+                        }
+                        if (u < kG && s == 0)
+                            mma_f16_zero(c[u % kG], qh.x, a1, qh.y, a3, b0, b1);
+                        else
+                            mma_f16(c[u % kG], s ? qh.z : qh.x, a1, s ? qh.w : qh.y, a3, b0, b1);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 sm = params(0, 8 * o + 2 * t + i);
+                    const float c0 = kQ == 2 ? c[0][i] + c[0][2 + i] : c[0][i];
+                    y[o][i] = fmaf(sm.x, c0, sm.y * qsum[0]);
+                    if constexpr (kG == 2) {
+                        const float c1 = kQ == 2 ? c[1][i] + c[1][2 + i] : c[1][i];
+                        y[o][i] = fmaf(sm.z, c1, fmaf(sm.w, qsum[1], y[o][i]));
+                    }
+                }
+            }
+            // ---- online softmax
+            if (seen != kFull) {
 #pragma unroll
                 for (int o = 0; o < 4; ++o)
 #pragma unroll
-                    for (int i = 0; i < kG; ++i) {
-                        const float2 sm = half_values(__shfl_sync(kFull, blk.par[kG + i], 8 * o + g));
-                        const float s = sm.x * fscale;
-                        float a = e[0][o] * s, b = e[1][o] * s;
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) pf[i][part][o] = transpose_8x8(half_pair(a, b));
-                        base[i][0] = fmaf(e[0][o], sm.y, base[i][0]);
-                        base[i][1] = fmaf(e[1][o], sm.y, base[i][1]);
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        if (!(seen >> (8 * o + 2 * t + i) & 1)) y[o][i] = -INFINITY;
             }
-            if (more) load_par(next, next_seen);
+            float sc;
+            {
+                float m = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1])),
+                                fmaxf(fmaxf(y[2][0], y[2][1]), fmaxf(y[3][0], y[3][1])));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+                m = fmaxf(M, m * kq);
+                const float ref = m == -INFINITY ? 0.f : m;
+                sc = ex2(M - ref);
+                M = m;
+                float z = 0.f;
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        y[o][i] = ex2(fmaf(y[o][i], kq, -ref));
+                        z += y[o][i];
+                    }
+                Z = fmaf(Z, sc, z);
+            }
+
+            // ---- the weights times V's scales: A operand, rows 0 .. 7 and (what fp16 left) 8 .. 15
+            uint32_t pa[kG][4][2];  // [group][octet][part]
+#pragma unroll
+            for (int i = 0; i < kG; ++i) base[i] *= sc;
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+                const float4 u = params(1, 8 * o + 2 * t), v = params(1, 8 * o + 2 * t + 1);
+                base[0] = fmaf(y[o][0], u.y, fmaf(y[o][1], v.y, base[0]));
+                float a = y[o][0] * u.x, b = y[o][1] * v.x;
+                pa[0][o][0] = half_pair(a, b);
+                pa[0][o][1] = half_pair(a, b);
+                if constexpr (kG == 2) {
+                    base[1] = fmaf(y[o][0], u.w, fmaf(y[o][1], v.w, base[1]));
+                    a = y[o][0] * u.z, b = y[o][1] * v.z;
+                    pa[1][o][0] = half_pair(a, b);
+                    pa[1][o][1] = half_pair(a, b);
+                }
+            }
+            __syncwarp();  // the parameters are read: the next block's may be written
+            if (more) load_k(next, next_seen);
 
             // ---- O += (e s) n, tile by tile
+            const float2 sco = make_float2(sc * lower, sc * lower);
 #pragma unroll
-            for (int i = 0; i < kW / 2; ++i) {
-                // pairs of keys: low and high halves of the word, octet by octet
-                uint32_t lo[4], hi[4];
+            for (int i = 0; i < kW / 2; ++i)
 #pragma unroll
-                for (int o = 0; o < 4; ++o) {
-                    lo[o] = __byte_perm(blk.v[o][0][i], blk.v[o][1][i], 0x5410);
-                    hi[o] = __byte_perm(blk.v[o][0][i], blk.v[o][1][i], 0x7632);
-                }
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pr[4];  // 4 nibbles of keys 8 o + 2t (low half) and + 1 (high half)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int sh8 = (q & 1) * 8;
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int o = 0; o < 4; ++o) pr[o] = __byte_perm(vc[o][0][i], vc[o][1][i], half ? 0x7632 : 0x5410);
 #pragma unroll
-                    for (int ks = 0; ks < 2; ++ks) {
-                        const uint32_t a = (q < 2 ? lo : hi)[2 * ks] >> sh8, b = (q < 2 ? lo : hi)[2 * ks + 1] >> sh8;
-                        const uint32_t frag[4] = {a & kLo, a & kHi, b & kLo, b & kHi};
+                    for (int s = 0; s < 2; ++s) {
+                        if (s)
 #pragma unroll
-                        for (int part = 1; part >= 0; --part)
-                            mma_f16_16816(acc, frag, pf[i % kG][part][2 * ks], pf[i % kG][part][2 * ks + 1]);
+                            for (int o = 0; o < 4; ++o) pr[o] >>= 8;
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi) {
+                            const uint32_t mask = hi ? kHi : kLo;
+                            const uint32_t(&a)[4][2] = pa[i % kG];
+                            float acc[4];
+                            mma_f16_zero(acc, a[0][0], a[0][1], a[1][0], a[1][1], pr[0] & mask, pr[1] & mask);
+                            mma_f16(acc, a[2][0], a[2][1], a[3][0], a[3][1], pr[2] & mask, pr[3] & mask);
+                            float(&o)[2] = O[8 * i + 4 * half + 2 * s + hi];
+                            const float2 sum = __fadd2_rn(make_float2(acc[0], acc[1]), make_float2(acc[2], acc[3]));
+                            const float2 r = __ffma2_rn(make_float2(o[0], o[1]), sco, sum);
+                            o[0] = r.x;
+                            o[1] = r.y;
+                        }
                     }
-                    float(&o)[4] = Ot[4 * i + q];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        o[j] = fmaf(o[j], sc[j], acc[j]);
-                        o[2 + j] = fmaf(o[2 + j], sc[j], acc[2 + j]);
-                    }
                 }
-            }
             if (more) load_v(next, next_seen);
 
             if (!same) {  // the stretch leaves the head
-                const bool whole = head.u0 >= x_first && head.u0 + head.nb <= w.x_end;
-                close(head, whole, 2 * warp + (more ? 0 : 1));
+                close(head, head.began && last, 2 * warp + (more ? 0 : 1));
                 reset();
                 fresh = true;
-                head = w.head;
+                head = Owner(w);
             }
             seen = next_seen;
         }
     }
-    float *room = reinterpret_cast<float *>(smem);  // the pieces are consumed when it is written
     join_pieces<NW, D>(
-        sp, sh, w, [&](int slot) { return const_cast<const float *>(pieces) + size_t(slot) * GT * D; }, room,
-        room + kSplitCtaBound * GT);
+        sp, sh, [&](int slot) { return const_cast<const float *>(pieces) + size_t(slot) * GT * D; },
+        reinterpret_cast<float *>(smem));  // the pieces are consumed when it is written
 }
 
 template <int D, typename Q, int GT>
 cudaError_t launch(const SplitParams &sp, cudaStream_t stream, const Timing &tm) {
-    using Geom = Kv4Geom<D, GT>;
+    using Geom = Kv4Geom<D, Q, GT>;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

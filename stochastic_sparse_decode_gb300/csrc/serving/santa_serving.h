@@ -57,7 +57,7 @@ struct SplitParams {
     float2 *part_mz;           // [CTAs][2][G] (M, Z) of a CTA's first and last head, where others share it
     float *part;               // [CTAs][2][G][D] the unnormalised sums
 };
-constexpr int kSplitCtaBound = 512;  // CTAs of a split launch at most (the workspace is sized for it)
+constexpr int kSplitCtaBound = 160;  // CTAs of a split launch at most (the workspace is sized for it)
 cudaError_t launch_window(const SplitParams &p, int dtype, cudaStream_t stream, const Timing &tm);
 cudaError_t launch_kv4(const SplitParams &p, int dtype, cudaStream_t stream, const Timing &tm);
 

@@ -37,7 +37,7 @@ __device__ __forceinline__ float ex2(float x) {
 struct Head {
     int b, kvh, nb;
     long long u0;
-    long long start;  // the sequence's first row (contiguous cache)
+    int start;        // the sequence's first row (contiguous cache; rows fit 31 bits)
     Visible vis;
     int nsb, wb0;     // sink blocks; the window's first block
     __device__ __forceinline__ int first_key(int n) const { return kBlock * (n < nsb ? n : wb0 + n - nsb); }
@@ -58,19 +58,26 @@ __device__ __forceinline__ void set_blocks(Head &h, int L, const SplitParams &sp
 }
 template <bool kPaged>
 __device__ __forceinline__ void load_head(Head &h, const SplitParams &sp, int b) {
+    long long start;
     h.b = b;
-    set_blocks(h, seq_bounds<kPaged>(sp.p, b, &h.start), sp);
+    set_blocks(h, seq_bounds<kPaged>(sp.p, b, &start), sp);
+    h.start = int(start);
 }
 
+// a / b for a >= 0, b > 0: by 32 bits where they fit (the 64-bit division is a subroutine).
+__device__ __forceinline__ long long divide(long long a, int b) {
+    return a >> 31 ? a / b : (long long)(unsigned(a) / unsigned(b));
+}
 // Stretch c of `parts` equal ones of X units starts at: (the first X mod parts are one longer)
 __device__ __forceinline__ long long stretch_start(long long X, int parts, int c) {
-    const long long q = X / parts, r = X - q * parts;
+    const long long q = divide(X, parts), r = X - q * parts;
     return q * c + (c < r ? c : r);
 }
 // The stretch that unit x lies in.
 __device__ __forceinline__ int stretch_of(long long X, int parts, long long x) {
-    const long long q = X / parts, r = X - q * parts, big = r * (q + 1);
-    return int(x < big ? x / (q + 1) : r + (x - big) / (q > 0 ? q : 1));
+    const long long q = divide(X, parts), r = X - q * parts, big = r * (q + 1);
+    if (q >> 30) return int(x < big ? x / (q + 1) : r + (x - big) / q);
+    return x < big ? int(divide(x, int(q) + 1)) : int(r + divide(x - big, q > 0 ? int(q) : 1));
 }
 
 // What a CTA's warps share.
@@ -79,8 +86,13 @@ struct SplitShared {
     float M[2 * NW][kMaxGroup], Z[2 * NW][kMaxGroup];  // pieces 2w (first head of warp w), 2w + 1 (last)
     long long u0[2 * NW];                              // the piece's head; -1: no piece
     int b[2 * NW], kvh[2 * NW], nb[2 * NW];
+    float coef[2 * NW][kMaxGroup];                     // weight of a piece in its head's sum
+    int list[2 * NW + 1];                              // the pieces there are, in order
+    int begin[2 * NW + 1];                             // where in `list` each head's pieces begin
     long long inc_u0[2];                               // the CTA's heads that others share: first, last
-    int inc_b[2], inc_kvh[2], inc_nb[2], inc_parts[2], last[2];
+    int inc_b[2], inc_kvh[2], inc_nb[2], inc_first[2], inc_parts[2], last[2];
+    long long X, cta0, cta1;                           // units of the batch; the CTA's stretch
+    int ctas;                                          // CTAs that have a stretch
     long long x0[NW];                                  // plan of a large batch: where the warps start
     long long prefix[NW];
     int start_b[NW];
@@ -89,13 +101,22 @@ struct SplitShared {
 
 // A warp's place in the walk.
 struct Walk {
-    long long x, x_end;     // next unit, end of the stretch
-    long long cta0, cta1;   // the CTA's stretch
-    long long X;
-    int ctas;               // CTAs that have a stretch
-    int n;                  // block of `head`
+    int left;     // units of the stretch, this one included
+    int n;        // block of `head`
+    int key0;     // its first key
+    int in_page;  // paged: where in its page the block begins
+    int row;      // its first cache row; -1: a bad page id (flagged), its keys are dropped
+    bool began;   // `head` begins in this stretch
     Head head;
 };
+
+// The row of block w.n, by the page table.
+template <bool kPaged>
+__device__ __forceinline__ void place(const SplitParams &sp, Walk &w) {
+    w.key0 = w.head.first_key(w.n);
+    w.row = int(key_row<kPaged>(sp.p, w.head.b, w.head.start, w.key0));
+    if constexpr (kPaged) w.in_page = w.key0 % sp.p.page_size;
+}
 
 __device__ __forceinline__ void zero_row(const Params &p, int b) {
     float4 *o = reinterpret_cast<float4 *>(p.out + size_t(b) * p.Hq * p.D);
@@ -103,27 +124,35 @@ __device__ __forceinline__ void zero_row(const Params &p, int b) {
 }
 
 // Finds the warp's stretch and its first unit; zeroes the rows of sequences without a key
-// (each by one CTA).  False: the warp has no unit.  Every thread of the CTA calls it.
+// (each by one CTA).  1: the walk stands on the warp's first unit; 0: the warp has none; -1: the
+// CTA has none.  Every thread of the CTA calls it.
 template <int NW, bool kPaged>
-__device__ __forceinline__ bool plan_walk(const SplitParams &sp, SplitShared<NW> &sh, Walk &w) {
+__device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> &sh, Walk &w) {
     const Params &p = sp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long total = 0, prefix = 0;
+    long long total = 0, prefix = 0, x = 0;
     int b = -1;
+    w.left = 0;
     auto ranges = [&]() {
-        w.X = total * p.Hkv;
-        const long long most = (w.X + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
-        w.ctas = most < (long long)gridDim.x ? int(most) : int(gridDim.x);
-        if ((int)blockIdx.x >= w.ctas) {
-            w.x = w.x_end = w.cta0 = w.cta1 = w.X;
-            return;
+        const long long X = total * p.Hkv, most = (X + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
+        const int ctas = most < (long long)gridDim.x ? int(most) : int(gridDim.x);
+        long long cta0 = X, cta1 = X;
+        if ((int)blockIdx.x < ctas) {
+            cta0 = stretch_start(X, ctas, blockIdx.x);
+            cta1 = stretch_start(X, ctas, blockIdx.x + 1);
+            const long long from = stretch_start(cta1 - cta0, NW, warp);
+            x = cta0 + from;
+            w.left = int(stretch_start(cta1 - cta0, NW, warp + 1) - from);
         }
-        w.cta0 = stretch_start(w.X, w.ctas, blockIdx.x);
-        w.cta1 = stretch_start(w.X, w.ctas, blockIdx.x + 1);
-        const int len = int(w.cta1 - w.cta0);
-        w.x = w.cta0 + stretch_start(len, NW, warp);
-        w.x_end = w.cta0 + stretch_start(len, NW, warp + 1);
+        if (threadIdx.x == 0) {
+            sh.X = X;
+            sh.cta0 = cta0;
+            sh.cta1 = cta1;
+            sh.ctas = ctas;
+        }
+        return ctas;
     };
+    int ctas;
     if (p.B <= 128) {  // every warp scans for itself: no barrier
         int nb[4];
         long long end[4];
@@ -152,12 +181,12 @@ __device__ __forceinline__ bool plan_walk(const SplitParams &sp, SplitShared<NW>
                 total = __shfl_sync(kFull, end[k], 31);
             }
         }
-        ranges();
-        if (w.x < w.x_end) {
+        ctas = ranges();
+        if (w.left > 0) {
 #pragma unroll
             for (int k = 3; k >= 0; --k)
                 if (32 * k < p.B) {
-                    const unsigned past = __ballot_sync(kFull, 32 * k + lane < p.B && end[k] * p.Hkv > w.x);
+                    const unsigned past = __ballot_sync(kFull, 32 * k + lane < p.B && end[k] * p.Hkv > x);
                     if (past) {
                         const int l = __ffs(past) - 1;
                         b = 32 * k + l;
@@ -193,9 +222,9 @@ __device__ __forceinline__ bool plan_walk(const SplitParams &sp, SplitShared<NW>
             block_scan(h.nb, &all);
             total += all;
         }
-        ranges();
+        ctas = ranges();
         if (lane == 0) {
-            sh.x0[warp] = w.x < w.x_end ? w.x : -1;
+            sh.x0[warp] = w.left > 0 ? x : -1;
             sh.start_b[warp] = -1;
         }
         long long carry = 0;
@@ -225,37 +254,68 @@ __device__ __forceinline__ bool plan_walk(const SplitParams &sp, SplitShared<NW>
         b = sh.start_b[warp];
         prefix = sh.prefix[warp];
     }
-    if (w.x >= w.x_end || b < 0) {
-        w.x = w.x_end;
-        return false;
+    if ((int)blockIdx.x >= ctas) return -1;
+    if (w.left <= 0 || b < 0) {
+        w.left = 0;
+        return 0;
     }
     load_head<kPaged>(w.head, sp, b);
-    const long long rem = w.x - prefix * p.Hkv;
-    w.head.kvh = int(rem / w.head.nb);
+    const long long rem = x - prefix * p.Hkv;
+    w.head.kvh = int(divide(rem, w.head.nb));
     w.n = int(rem - (long long)w.head.kvh * w.head.nb);
-    w.head.u0 = w.x - w.n;
-    return true;
+    w.head.u0 = x - w.n;
+    w.began = w.n == 0;
+    place<kPaged>(sp, w);
+    return 1;
 }
 
 // Moves to the next unit; false at the stretch's end.
 template <bool kPaged>
 __device__ __forceinline__ bool next_unit(const SplitParams &sp, Walk &w) {
-    if (++w.x >= w.x_end) return false;
-    if (++w.n < w.head.nb) return true;
+    if (--w.left <= 0) return false;
+    if (++w.n < w.head.nb) {
+        if (w.n != w.head.nsb) {  // the next block of the sequence
+            w.key0 += kBlock;
+            if constexpr (!kPaged) {
+                w.row += kBlock;
+                return true;
+            } else {
+                w.in_page += kBlock;
+                if (w.in_page < sp.p.page_size) {
+                    if (w.row >= 0) w.row += kBlock;
+                    return true;
+                }
+            }
+        }
+        place<kPaged>(sp, w);
+        return true;
+    }
     w.n = 0;
-    w.head.u0 = w.x;
-    if (++w.head.kvh < sp.p.Hkv) return true;
-    w.head.kvh = 0;
-    int b = w.head.b;
-    do {
-        load_head<kPaged>(w.head, sp, ++b);
-    } while (w.head.nb == 0 && b + 1 < sp.p.B);
+    w.head.u0 += w.head.nb;
+    w.began = true;
+    if (++w.head.kvh >= sp.p.Hkv) {
+        w.head.kvh = 0;
+        int b = w.head.b;
+        do {
+            load_head<kPaged>(w.head, sp, ++b);
+        } while (w.head.nb == 0 && b + 1 < sp.p.B);
+    }
+    place<kPaged>(sp, w);
     return true;
 }
 
+// The head that a warp's state belongs to.
+struct Owner {
+    long long u0;
+    int b, kvh, nb;
+    bool began;  // within the stretch
+    __device__ __forceinline__ Owner(const Walk &w)
+        : u0(w.head.u0), b(w.head.b), kvh(w.head.kvh), nb(w.head.nb), began(w.began) {}
+};
+
 // Notes that piece `slot` belongs to `h`.  One lane.
 template <int NW>
-__device__ __forceinline__ void note_piece(SplitShared<NW> &sh, int slot, const Head &h) {
+__device__ __forceinline__ void note_piece(SplitShared<NW> &sh, int slot, const Owner &h) {
     sh.u0[slot] = h.u0;
     sh.b[slot] = h.b;
     sh.kvh[slot] = h.kvh;
@@ -263,60 +323,78 @@ __device__ __forceinline__ void note_piece(SplitShared<NW> &sh, int slot, const 
 }
 
 // Joins the CTA's pieces, and the parts of the heads that this CTA completes.  `piece(slot)`
-// is the address of a piece's sums [G][D] in shared memory (sh.M, sh.Z beside them);
-// `coef` room for ctas * G floats there, not overlapping the pieces' use after the barrier
-// that follows them.  Every thread of the CTA calls it, after its warp's pieces are written.
+// is the address of a piece's sums [G][D] in shared memory (sh.M, sh.Z beside them); `room`
+// is shared memory for kSplitCtaBound * G floats and a float4 per thread, which may overlap
+// the pieces.  Every thread of the CTA calls it, after its warp's pieces are written.
 template <int NW, int D, typename PieceAddr>
-__device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<NW> &sh, const Walk &w, PieceAddr piece,
-                                            float *coef, float *red) {
+__device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<NW> &sh, PieceAddr piece,
+                                            float *room) {
+    static_assert(2 * NW <= 32, "a lane per piece");
     const Params &p = sp.p;
-    constexpr int kE = D / 32, NT = NW * 32;
+    constexpr int NT = NW * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.G;
     if (threadIdx.x < 2) sh.inc_u0[threadIdx.x] = -1;
     __syncthreads();
-    // one (group of pieces of a head, query head) per warp at a time; a group begins at its first piece
-    for (int item = warp; item < 2 * NW * G; item += NW) {
-        const int i = item / G, h = item - i * G;
-        const long long u0 = sh.u0[i];
-        if (u0 < 0) continue;
-        const bool in = lane < 2 * NW && sh.u0[lane < 2 * NW ? lane : 0] == u0;
-        const unsigned members = __ballot_sync(kFull, in);
-        if (__ffs(members) - 1 != i) continue;
-        float m = in ? sh.M[lane][h] : -INFINITY;
+    const long long cta0 = sh.cta0, cta1 = sh.cta1;
+    // the pieces there are, and where each head's begin (every warp finds the same)
+    const long long my_u0 = lane < 2 * NW ? sh.u0[lane] : -1;
+    const unsigned valid = __ballot_sync(kFull, my_u0 >= 0);
+    const unsigned mates = __match_any_sync(kFull, my_u0) & valid;
+    const unsigned heads = __ballot_sync(kFull, my_u0 >= 0 && __ffs(mates) - 1 == lane);
+    const int n_heads = __popc(heads);
+    if (warp == 0) {
+        const int at = __popc(valid & ((1u << lane) - 1));
+        if (my_u0 >= 0) sh.list[at] = lane;
+        if (heads >> lane & 1) sh.begin[__popc(heads & ((1u << lane) - 1))] = at;
+        if (lane == 0) sh.begin[n_heads] = __popc(valid);
+    }
+    for (int item = warp; item < n_heads * G; item += NW) {
+        const int k = item / G, h = item - k * G;
+        unsigned rest = heads;
+        for (int q = 0; q < k; ++q) rest &= rest - 1;
+        const int i = __ffs(rest) - 1;  // the head's first piece
+        const bool in = __shfl_sync(kFull, mates, i) >> lane & 1;
+        const long long u0 = __shfl_sync(kFull, my_u0, i);
+        const float m = in ? sh.M[lane][h] : -INFINITY;
         const float M = warp_max(m), Mref = M == -INFINITY ? 0.f : M;
-        const float c = in ? ex2(m - Mref) : 0.f;
+        float c = in ? ex2(m - Mref) : 0.f;
         const float Z = warp_sum(in ? sh.Z[lane][h] * c : 0.f);
-        float o[kE];
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = 0.f;
-        for (unsigned left = members; left; left &= left - 1) {
-            const int s = __ffs(left) - 1;
-            const float cs = __shfl_sync(kFull, c, s);
-            const float *src = piece(s) + h * D + lane * kE;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) o[e] = fmaf(cs, src[e], o[e]);
-        }
-        if (u0 >= w.cta0 && u0 + sh.nb[i] <= w.cta1) {  // nobody else has a part
-            const float inv = Z == 0.f ? 0.f : 1.f / Z;
-            float *dst = p.out + (size_t(sh.b[i]) * p.Hq + sh.kvh[i] * G + h) * D + lane * kE;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) dst[e] = Z == 0.f ? 0.f : o[e] * inv;
-        } else {
-            const int part = u0 <= w.cta0 ? 0 : 1;
-            const size_t at = (size_t(blockIdx.x) * 2 + part) * G + h;
-            float *dst = sp.part + at * D + lane * kE;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) __stcg(dst + e, o[e]);
-            if (lane == 0) {
-                __stcg(sp.part_mz + at, make_float2(M, Z));
-                if (h == 0) {
-                    sh.inc_u0[part] = u0;
-                    sh.inc_b[part] = sh.b[i];
-                    sh.inc_kvh[part] = sh.kvh[i];
-                    sh.inc_nb[part] = sh.nb[i];
-                }
+        if (u0 >= cta0 && u0 + sh.nb[i] <= cta1) {  // nobody else has a part
+            c = Z == 0.f ? 0.f : c / Z;
+        } else if (lane == 0) {
+            const int part = u0 <= cta0 ? 0 : 1;
+            __stcg(sp.part_mz + (size_t(blockIdx.x) * 2 + part) * G + h, make_float2(M, Z));
+            if (h == 0) {
+                sh.inc_u0[part] = u0;
+                sh.inc_b[part] = sh.b[i];
+                sh.inc_kvh[part] = sh.kvh[i];
+                sh.inc_nb[part] = sh.nb[i];
             }
-            __threadfence();
+        }
+        if (in) sh.coef[lane][h] = c;
+    }
+    __syncthreads();
+    const int cols = G * D / 4;  // float4 columns of a head's sums
+    for (int task = threadIdx.x; task < n_heads * cols; task += NT) {
+        const int k = task / cols, col = task - k * cols, h = col / (D / 4);
+        const int j0 = sh.begin[k], j1 = sh.begin[k + 1], i = sh.list[j0];
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int j = j0; j < j1; ++j) {
+            const int s = sh.list[j];
+            const float c = sh.coef[s][h];
+            const float4 v = reinterpret_cast<const float4 *>(piece(s))[col];
+            o.x = fmaf(c, v.x, o.x);
+            o.y = fmaf(c, v.y, o.y);
+            o.z = fmaf(c, v.z, o.z);
+            o.w = fmaf(c, v.w, o.w);
+        }
+        const long long u0 = sh.u0[i];
+        if (u0 >= cta0 && u0 + sh.nb[i] <= cta1) {
+            reinterpret_cast<float4 *>(p.out + (size_t(sh.b[i]) * p.Hq + sh.kvh[i] * G) * D)[col] = o;
+        } else {
+            const int part = u0 <= cta0 ? 0 : 1;
+            __stcg(reinterpret_cast<float4 *>(sp.part + (size_t(blockIdx.x) * 2 + part) * G * D) + col, o);
         }
     }
     __syncthreads();
@@ -324,77 +402,108 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
         const int k = threadIdx.x;
         sh.last[k] = 0;
         if (sh.inc_u0[k] >= 0) {
-            const int first = stretch_of(w.X, w.ctas, sh.inc_u0[k]);
-            const int parts = stretch_of(w.X, w.ctas, sh.inc_u0[k] + sh.inc_nb[k] - 1) - first + 1;
+            const int first = stretch_of(sh.X, sh.ctas, sh.inc_u0[k]);
+            const int parts = stretch_of(sh.X, sh.ctas, sh.inc_u0[k] + sh.inc_nb[k] - 1) - first + 1;
+            sh.inc_first[k] = first;
             sh.inc_parts[k] = parts;
+            // the CTA's part is visible (the barrier above, this fence) before it is counted
             __threadfence();
             unsigned *cnt = sp.cnt + size_t(sh.inc_b[k]) * p.Hkv + sh.inc_kvh[k];
             if (atomicAdd(cnt, 1u) == unsigned(parts - 1)) {
                 sh.last[k] = 1;
                 *cnt = 0u;
+                __threadfence();  // the others' parts are read after their counts
             }
-            __threadfence();
         }
     }
     __syncthreads();
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         if (!sh.last[k]) continue;
-        const int parts = sh.inc_parts[k], first = stretch_of(w.X, w.ctas, sh.inc_u0[k]);
-        // part c of the head: the head is the first CTA's first one only if it starts its stretch
-        const int slot0 = sh.inc_u0[k] <= stretch_start(w.X, w.ctas, first) ? 0 : 1;
+        const int parts = sh.inc_parts[k], first = sh.inc_first[k];
+        // the head is its first CTA's first one only if it starts that CTA's stretch
+        const int slot0 = sh.inc_u0[k] <= stretch_start(sh.X, sh.ctas, first) ? 0 : 1;
         auto index = [&](int c) { return (size_t(first + c) * 2 + (c == 0 ? slot0 : 0)) * G; };
-        for (int h = warp; h < G; h += NW) {
-            float M = -INFINITY, Z = 0.f;
-            for (int c = lane; c < parts; c += 32) M = fmaxf(M, __ldcg(sp.part_mz + index(c) + h).x);
-            M = warp_max(M);
-            const float Mref = M == -INFINITY ? 0.f : M;
-            for (int c = lane; c < parts; c += 32) {
-                const float2 mz = __ldcg(sp.part_mz + index(c) + h);
-                const float f = ex2(mz.x - Mref);
-                coef[c * G + h] = f;
-                Z = fmaf(mz.y, f, Z);
+        // groups of threads take the parts in turn, a float4 column per thread (cols of them in
+        // passes of at most NT); their first rows are requested before the coefficients are known
+        for (int col0 = 0; col0 < cols; col0 += NT) {
+            const int width = min(cols - col0, NT), groups = NT / width;
+            const int grp = threadIdx.x / width, col = col0 + threadIdx.x - grp * width;
+            const bool on = grp < groups;
+            constexpr int kAhead = 8;
+            float4 v[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int c = grp + u * groups;
+                v[u] = on && c < parts ? __ldcg(reinterpret_cast<const float4 *>(sp.part + index(c) * D) + col)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            Z = warp_sum(Z);
-            __syncwarp();
-            for (int c = lane; c < parts; c += 32) coef[c * G + h] = Z == 0.f ? 0.f : coef[c * G + h] / Z;
-        }
-        __syncthreads();
-        // the sums: groups of G D / 4 threads take the parts in turn, then the groups in order
-        const int cols = G * D / 4, groups = NT >= cols ? NT / cols : 1;
-        for (int c0 = 0; c0 < cols; c0 += NT) {
-            const int col = NT >= cols ? threadIdx.x % cols : c0 + threadIdx.x, grp = NT >= cols ? threadIdx.x / cols : 0;
-            const bool on = grp < groups && col < cols;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (on) {
-                const int h = col * 4 / D;
-#pragma unroll 8
-                for (int c = grp; c < parts; c += groups) {
-                    const float f = coef[c * G + h];
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(sp.part + index(c) * D) + col);
-                    acc.x = fmaf(f, v.x, acc.x);
-                    acc.y = fmaf(f, v.y, acc.y);
-                    acc.z = fmaf(f, v.z, acc.z);
-                    acc.w = fmaf(f, v.w, acc.w);
+            float *coef = room;
+            for (int h = warp; h < G && col0 == 0; h += NW) {
+                constexpr int kPer = (kSplitCtaBound + 31) / 32;
+                float2 mz[kPer];
+                float M = -INFINITY, Z = 0.f;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    const int c = lane + 32 * u;
+                    mz[u] = c < parts ? __ldcg(sp.part_mz + index(c) + h) : make_float2(-INFINITY, 0.f);
+                    M = fmaxf(M, mz[u].x);
+                }
+                M = warp_max(M);
+                const float Mref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    mz[u].x = ex2(mz[u].x - Mref);
+                    Z = fmaf(mz[u].y, mz[u].x, Z);
+                }
+                Z = warp_sum(Z);
+                const float inv = Z == 0.f ? 0.f : 1.f / Z;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    const int c = lane + 32 * u;
+                    if (c < parts) coef[c * G + h] = Z == 0.f ? 0.f : mz[u].x * inv;
                 }
             }
-            float4 *r4 = reinterpret_cast<float4 *>(red);
+            __syncthreads();
+            const int h = col / (D / 4);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int c = grp + u * groups;
+                    const float f = c < parts ? coef[c * G + h] : 0.f;
+                    acc.x = fmaf(f, v[u].x, acc.x);
+                    acc.y = fmaf(f, v[u].y, acc.y);
+                    acc.z = fmaf(f, v[u].z, acc.z);
+                    acc.w = fmaf(f, v[u].w, acc.w);
+                }
+#pragma unroll 8
+                for (int c = grp + kAhead * groups; c < parts; c += groups) {
+                    const float f = coef[c * G + h];
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(sp.part + index(c) * D) + col);
+                    acc.x = fmaf(f, x.x, acc.x);
+                    acc.y = fmaf(f, x.y, acc.y);
+                    acc.z = fmaf(f, x.z, acc.z);
+                    acc.w = fmaf(f, x.w, acc.w);
+                }
+            }
+            float4 *red = reinterpret_cast<float4 *>(room + kSplitCtaBound * kMaxGroup);
             if (groups > 1) {
-                if (on) r4[grp * cols + col] = acc;
+                if (on && grp > 0) red[(grp - 1) * width + col - col0] = acc;
                 __syncthreads();
-                if (on && grp == 0)
+                if (grp == 0)
                     for (int g = 1; g < groups; ++g) {
-                        const float4 v = r4[g * cols + col];
-                        acc.x += v.x;
-                        acc.y += v.y;
-                        acc.z += v.z;
-                        acc.w += v.w;
+                        const float4 x = red[(g - 1) * width + col - col0];
+                        acc.x += x.x;
+                        acc.y += x.y;
+                        acc.z += x.z;
+                        acc.w += x.w;
                     }
             }
-            if (on && grp == 0)
+            if (grp == 0)
                 reinterpret_cast<float4 *>(p.out + (size_t(sh.inc_b[k]) * p.Hq + sh.inc_kvh[k] * G) * D)[col] = acc;
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 

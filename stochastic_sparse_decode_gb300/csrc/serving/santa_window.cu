@@ -64,7 +64,7 @@ struct WindowGeom {
     // after the walk the buffers hold a warp's last piece; the joined heads' coefficients
     // and partial sums take the room of the first pieces and of other buffers
     static_assert(size_t(GT) * D * 4 <= size_t(2) * kBytes, "a piece fits a warp's buffers");
-    static_assert(size_t(kSplitCtaBound) * GT * 4 + size_t(kWarps) * 32 * 16 <= kFirst, "room to join");
+    static_assert(size_t(kSplitCtaBound) * kMaxGroup * 4 + size_t(kWarps) * 32 * 16 <= kFirst, "room to join");
 };
 
 template <typename T, int D, int GT, bool kPaged>
@@ -100,14 +100,10 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
     pdl_launch_dependents();
 
     Walk w;
-    const bool any = plan_walk<NW, kPaged>(sp, sh, w);
-    if ((int)blockIdx.x >= w.ctas) return;
+    const int any = plan_walk<NW, kPaged>(sp, sh, w);
+    if (any < 0) return;
 
-    // The block at the walk's place: its first cache row (-1: a bad page, dropped) and first key.
-    auto block_row = [&](int key0) {
-        return key_row<kPaged>(p, w.head.b, w.head.start, key0);
-    };
-    auto issue = [&](int which, long long row, int kvh) {
+    auto issue = [&](int which, int row, int kvh) {
         if (lane != 0) return;
         uint64_t *bar = &bars[which];
         if (row >= 0) {
@@ -116,7 +112,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
             mbar_arrive_expect_tx(bar, WG::kBytes);
 #pragma unroll
             for (int bx = 0; bx < Geo::kBoxes; ++bx)
-                tma_load_3d(dst + bx * kChunkBoxBytes, which ? &vmap : &kmap, bar, bx * Geo::kBoxElems, kvh, int(row));
+                tma_load_3d(dst + bx * kChunkBoxBytes, which ? &vmap : &kmap, bar, bx * Geo::kBoxElems, kvh, row);
         } else {
             mbar_arrive(bar);
         }
@@ -141,7 +137,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
             for (int e = 0; e < kE; ++e) O[h][e] = 0.f;
     };
     // Closes the state for `head`: final outputs (kind 0), or piece `slot` with its sums at o.
-    auto close = [&](const Head &head, bool final, int slot, float *o) {
+    auto close = [&](const Owner &head, bool final, int slot, float *o) {
         if constexpr (kMma) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -184,26 +180,21 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
 
     const float scale2 = p.scale * 1.4426950408889634f;  // logits in base 2
     bool failed = false, k_flying = true;  // k_flying: the K barrier's phase is still to complete
-    if (any) {
-        Head head = w.head;  // of the block being computed; w runs one block ahead
-        int key0 = head.first_key(w.n);
-        long long row = block_row(key0);
+    if (any > 0) {
+        Owner head(w);  // of the block being computed; w runs one block ahead
+        Visible vis = w.head.vis;
+        int key0 = w.key0;
+        int row = w.row;
         issue(0, row, head.kvh);
         issue(1, row, head.kvh);
-        const long long x_first = w.x;
         uint32_t qf[kMma ? D / 16 : 1][2];
         uint32_t phK = 0, phV = 0;
         bool fresh = true;  // the state is empty and q not loaded
         reset();
         for (bool more = true; more;) {
+            const bool last = w.n + 1 == head.nb;  // the block is its head's last
             more = next_unit<kPaged>(sp, w);
             const bool same = more && w.head.u0 == head.u0;
-            int next_key0 = 0;
-            long long next_row = -1;
-            if (more) {
-                next_key0 = w.head.first_key(w.n);
-                next_row = block_row(next_key0);
-            }
             if (fresh && kMma) {
                 // lane (g, t): dimensions 16 ks + 2t, +1 and 16 ks + 2t + 8, +9 of head g
                 const uint32_t *qh = reinterpret_cast<const uint32_t *>(
@@ -217,7 +208,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
             fresh = false;
             auto seen = [&](int r) {
                 const int key = key0 + r;
-                return key < head.vis.L && (key < head.vis.s || key >= head.vis.lo);
+                return key < vis.L && (key < vis.s || key >= vis.lo);
             };
             if (!mbar_wait(&bars[0], phK)) {
                 failed = true;
@@ -250,7 +241,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                 }
             }
             __syncwarp();
-            if (more) issue(0, next_row, w.head.kvh);  // the K buffer is free
+            if (more) issue(0, w.row, w.head.kvh);  // the K buffer is free
             k_flying = more;
 
             uint32_t pf[3][4];  // weights, part by part: keys 8 o + 2t, + 1 of head g
@@ -312,8 +303,8 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
             }
             phV ^= 1u;
             if (row >= 0) {
-                const bool partial = key0 + kBlock > head.vis.L ||
-                                     (key0 < head.vis.lo && key0 + kBlock > head.vis.s);
+                const bool partial = key0 + kBlock > vis.L ||
+                                     (key0 < vis.lo && key0 + kBlock > vis.s);
                 if (partial) {  // rows that the query must not see: zeros
                     for (int i = lane; i < kBlock * Geo::kBoxes * 8; i += 32) {
                         const int r = (i >> 3) % kBlock, bx = (i >> 3) / kBlock;
@@ -373,11 +364,10 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                 }
             }
             __syncwarp();
-            if (more) issue(1, next_row, w.head.kvh);  // the V buffer is free
+            if (more) issue(1, w.row, w.head.kvh);  // the V buffer is free
 
             if (!same) {  // the stretch leaves the head
-                const bool whole = head.u0 >= x_first && head.u0 + head.nb <= w.x_end;
-                if (whole)
+                if (head.began && last)
                     close(head, true, 0, nullptr);
                 else if (more)
                     close(head, false, 2 * warp, first_piece + size_t(warp) * GT * D);
@@ -385,10 +375,11 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                     close(head, false, 2 * warp + 1, reinterpret_cast<float *>(kbuf));
                 reset();
                 fresh = true;
-                head = w.head;
+                head = Owner(w);
+                vis = w.head.vis;
             }
-            key0 = next_key0;
-            row = next_row;
+            key0 = w.key0;
+            row = w.row;
         }
         if (failed) {
             // SANTA_ERR_TIMEOUT, location code 4; wait, bounded, for the copies in flight
@@ -406,12 +397,12 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
     // the joined heads' coefficients lie in the warps' buffers, whose pieces are consumed by then
     float *room = reinterpret_cast<float *>(smem);
     join_pieces<NW, D>(
-        sp, sh, w,
+        sp, sh,
         [&](int slot) {
             return slot & 1 ? reinterpret_cast<const float *>(smem + size_t(slot >> 1) * 2 * WG::kBytes)
                             : const_cast<const float *>(first_piece) + size_t(slot >> 1) * GT * D;
         },
-        room, room + kSplitCtaBound * GT);
+        room);
 }
 
 // Tensor map of a [rows][Hkv][d] cache: boxes of 128 bytes of one head's row x 32 rows.
