@@ -11,10 +11,11 @@
 // Queries and weights are the A operand (rows = heads), codes the B operand, so the logits
 // come out in the layout in which the weights go in, and a lane deals with one head.  A word
 // of K's codes is the B operand of two products (4 ands, 1 shift); two keys' words of V,
-// paired by byte permutes, those of eight (2 permutes, 8 ands, 2 shifts).  Nothing is staged
-// through shared memory but the rows' scales and minima, converted once by the lane that
-// has the key; codes go from global memory to registers, the next block's while the current
-// one is computed.
+// paired by byte permutes, those of eight (2 permutes, 8 ands, 2 shifts).  The rows' scales and
+// minima are converted once, by the lane that has the key, and shared through shared memory.
+// d = 128: a warp's blocks come by TMA (boxes of 32 records) into two buffers of its own.
+// d = 64: a record is 72 bytes, which TMA's strides cannot express; the codes go from global
+// memory to registers, the next block's while the current one is computed.
 //
 // Precision: q is scaled by a power of two per head to fit fp16 (a bf16 q is exact so; an
 // fp32 q is taken in two parts, 22 bits, the second in the A operand's rows 8 .. 15); the
@@ -26,6 +27,7 @@
 #include <cuda_fp16.h>
 
 #include "santa_split.cuh"
+#include "santa_stream.cuh"
 
 namespace santa {
 
@@ -69,36 +71,52 @@ constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
 template <int D, typename Q, int GT>
 struct Kv4Geom {
-    static constexpr int kWarps = 12;
+    static constexpr bool kTma = D == 128;
+    static constexpr int kQ = sizeof(Q) == 2 ? 1 : 2;        // fp16 parts of q
+    static constexpr int kWarps = kTma && (GT > 4 || kQ > 1) ? 12 : 16;
     static constexpr int kG = D / 64;
-    static constexpr int kQ = sizeof(Q) == 2 ? 1 : 2;       // fp16 parts of q
-    static constexpr int kParBytes = kBlock * kG * 16;      // a block's (scale, minimum) of K and of V in fp32
-    static constexpr int kQBytes = 32 * (D / 32) * 16 * kQ; // a warp's A operand of q
-    // shared memory: first and last pieces [kWarps][2][GT][D], q and parameters per warp, shared state
-    static constexpr size_t kQOff = size_t(kWarps) * 2 * GT * D * 4;
-    static constexpr size_t kParOff = kQOff + size_t(kWarps) * kQBytes;
-    static constexpr size_t kShared = kParOff + size_t(kWarps) * kParBytes;
+    static constexpr int kBuf = kTma ? kBlock * kv4_record(D) : 0;  // bytes of a block
+    static constexpr int kParBytes = kBlock * kG * 16;       // its (scale, minimum) of K and of V in fp32
+    static constexpr size_t kPiece = size_t(GT) * D * 4;
+    // shared memory: two buffers per warp (its last piece when the walk is over; d = 64: that piece
+    // alone), first pieces, parameters, mbarriers, shared state
+    static constexpr size_t kSlot = kTma ? 2 * size_t(kBuf) : kPiece;
+    static constexpr size_t kFirst = kWarps * kSlot;
+    static constexpr size_t kParOff = kFirst + kWarps * kPiece;
+    static constexpr size_t kBars = kParOff + size_t(kWarps) * kParBytes;
+    static constexpr size_t kShared = kBars + size_t(kWarps) * 16;
     static constexpr size_t kTotal = kShared + sizeof(SplitShared<kWarps>);
-    static_assert(size_t(kSplitCtaBound) * kMaxGroup * 4 + size_t(kWarps) * 32 * 16 <= kParOff, "room to join");
+    static_assert(kPiece <= kSlot && kSlot % 128 == 0, "a piece fits a warp's buffers");
+    static_assert(size_t(kSplitCtaBound) * kMaxGroup * 4 + size_t(kWarps) * 32 * 16 <= kBars, "room to join");
     static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
 template <int D, typename Q, int GT, bool kPaged>
-__global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(const __grid_constant__ SplitParams sp) {
+__global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
+    kv4_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ SplitParams sp) {
     using Geom = Kv4Geom<D, Q, GT>;
     constexpr int NW = Geom::kWarps, kG = Geom::kG, kQ = Geom::kQ;
+    constexpr bool kTma = Geom::kTma;
     constexpr int kW = D / 32;   // words of K's codes per key and lane; V: kW / 2
     constexpr int kTiles = D / 8;
     constexpr int kRec = kv4_record(D);
     const Params &p = sp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = p.G;
-    extern __shared__ __align__(16) unsigned char smem[];
-    float *pieces = reinterpret_cast<float *>(smem);  // [warp][first, last][GT][D]
-    uint4 *qa = reinterpret_cast<uint4 *>(smem + Geom::kQOff + warp * Geom::kQBytes);       // [word][part][lane]
-    float4 *par = reinterpret_cast<float4 *>(smem + Geom::kParOff + warp * Geom::kParBytes);  // see stage
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *buf = smem + warp * Geom::kSlot;
+    float *first_piece = reinterpret_cast<float *>(smem + Geom::kFirst);                    // [warp][GT][D]
+    float4 *par = reinterpret_cast<float4 *>(smem + Geom::kParOff + warp * Geom::kParBytes);  // see below
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Geom::kBars) + warp * 2;
     SplitShared<NW> &sh = *reinterpret_cast<SplitShared<NW> *>(smem + Geom::kShared);
-    if (lane < 2) sh.u0[2 * warp + lane] = -1;
+    if (lane < 2) {
+        sh.u0[2 * warp + lane] = -1;
+        if (kTma) mbar_init(&bars[lane], 1);
+    }
+    if (kTma) {
+        if (threadIdx.x == 0) prefetch_tensormap(&map);
+        fence_barrier_init();
+    }
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
@@ -107,27 +125,33 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
     const int any = plan_walk<NW, kPaged>(sp, sh, w);
     if (any < 0) return;
 
-    const uint32_t step = uint32_t(p.Hkv) * kRec;  // bytes from a key's record to the next key's
-    // a block's codes: K of keys 8 o + g (words kW t ..), V of keys 8 o + 2t + i (words kW / 2 g ..),
-    // and key `lane`'s pairs (scale, minimum): K's groups, then V's
-    uint32_t kc[4][kW], vc[4][2][kW / 2], pc[2 * kG];
-    // which keys of the walk's block the query sees, a bit each
-    auto seen_bits = [&]() {
-        const int key = w.key0 + lane;
-        const Visible &v = w.head.vis;
-        return __ballot_sync(kFull, w.row >= 0 && key < v.L && (key < v.s || key >= v.lo));
+    // d = 128: starts the copy of the walk's block into buffer i (a dropped block completes the
+    // buffer's phase with a plain arrive)
+    auto issue = [&](int i) {
+        if (lane != 0) return;
+        if (w.row >= 0) {
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&bars[i], Geom::kBuf);
+            tma_load_3d(buf + i * Geom::kBuf, &map, &bars[i], 0, w.heads[w.sel].kvh, w.row);
+        } else {
+            mbar_arrive(&bars[i]);
+        }
     };
-    auto record = [&]() { return sp.kv4 + ((size_t)(w.row < 0 ? 0 : w.row) * p.Hkv + w.head.kvh) * kRec; };
+    // the block's codes: K of keys 8 o + g (words kW t ..), V of keys 8 o + 2t + i (words kW / 2 g ..),
+    // and key `lane`'s pairs (scale, minimum): K's groups, then V's.  d = 64: from global memory,
+    // zeros for keys that the query must not see (rec: the block's first record).
+    const uint32_t step = kTma ? kRec : uint32_t(p.Hkv) * kRec;  // bytes from a key's record to the next key's
+    uint32_t kc[4][kW], vc[4][2][kW / 2], pc[2 * kG];
+    auto record = [&]() { return sp.kv4 + ((size_t)(w.row < 0 ? 0 : w.row) * p.Hkv + w.heads[w.sel].kvh) * kRec; };
     auto load_k = [&](const unsigned char *rec, unsigned seen) {
         const unsigned char *src = rec + g * step + t * (kW * 4);
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
-            const bool in = seen >> (8 * o + g) & 1;
-            if constexpr (kW == 4) {
-                const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-                kc[o][0] = x.x, kc[o][1] = x.y, kc[o][2] = x.z, kc[o][3] = x.w;
+            if constexpr (kTma) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                kc[o][0] = x.x, kc[o][1] = x.y, kc[o][kW - 2] = x.z, kc[o][kW - 1] = x.w;
             } else {
-                const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
+                const uint2 x = seen >> (8 * o + g) & 1 ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
                 kc[o][0] = x.x, kc[o][1] = x.y;
             }
             src += 8 * step;
@@ -139,13 +163,12 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
         for (int o = 0; o < 4; ++o) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const bool in = seen >> (8 * o + 2 * t + i) & 1;
                 const unsigned char *at = src + i * step;
-                if constexpr (kW == 4) {
-                    const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(at)) : make_uint2(0, 0);
-                    vc[o][i][0] = x.x, vc[o][i][1] = x.y;
+                if constexpr (kTma) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                    vc[o][i][0] = x.x, vc[o][i][kW / 2 - 1] = x.y;
                 } else {
-                    vc[o][i][0] = in ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
+                    vc[o][i][0] = seen >> (8 * o + 2 * t + i) & 1 ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
                 }
             }
             src += 8 * step;
@@ -153,10 +176,10 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
     };
     auto load_par = [&](const unsigned char *rec, unsigned seen) {
         const unsigned char *src = rec + lane * step + D;
-        const bool in = seen >> lane & 1;
-        if constexpr (kG == 2) {
-            const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-            pc[0] = x.x, pc[1] = x.y, pc[2] = x.z, pc[3] = x.w;
+        const bool in = seen >> lane & 1;  // the others' scales may be anything
+        if constexpr (kTma) {
+            const uint4 x = in ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+            pc[0] = x.x, pc[1] = x.y, pc[2 * kG - 2] = x.z, pc[2 * kG - 1] = x.w;
         } else {
             const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
             pc[0] = x.x, pc[1] = x.y;
@@ -176,7 +199,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) O[n][0] = O[n][1] = 0.f;
     };
-    auto close = [&](const Owner &head, bool final, int slot) {
+    auto close = [&](const Head &head, bool final, int slot) {
 #pragma unroll
         for (int x = 1; x < 4; x <<= 1) {
             Z += __shfl_xor_sync(kFull, Z, x);
@@ -185,7 +208,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
         }
         if (g < G) {
             float *dst = final ? p.out + (size_t(head.b) * p.Hq + head.kvh * G + g) * D
-                               : pieces + (size_t(slot) * GT + g) * D;
+                               : (slot & 1 ? reinterpret_cast<float *>(buf) : first_piece + size_t(warp) * GT * D) + g * D;
             const float inv = !final ? 1.f : Z == 0.f ? 0.f : 1.f / Z;
             const float f[2] = {16777216.f / fscale, 1048576.f / fscale};  // powers of two
 #pragma unroll
@@ -209,32 +232,39 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
     };
 
     if (any > 0) {
-        Owner head(w);  // of the block being computed; w runs one block ahead
-        unsigned seen = seen_bits();
-        {
+        int sel = w.sel;  // the head of the block being computed; w runs one block ahead
+        unsigned seen = seen_bits(w);
+        if constexpr (kTma) {
+            issue(0);
+        } else {
             const unsigned char *rec = record();
             load_par(rec, seen);
             load_k(rec, seen);
             load_v(rec, seen);
         }
+        uint32_t qf[kQ][kW][4];  // the A operand of q, see below
+        int cur = 0;             // the buffer of the block
+        uint32_t phase = 0;
         float qsum[kG], kq = 0.f;  // of head g: sum(q_g) and the logits' factor: x = kq y, base 2
-        bool fresh = true;
+        bool fresh = true, failed = false;
         reset();
         for (bool more = true; more;) {
-            const bool last = w.n + 1 == head.nb;  // the block is its head's last
-            more = next_unit<kPaged>(sp, w);
-            const bool same = more && w.head.u0 == head.u0;
+            const int n = w.n, moved = next_unit<kPaged>(sp, w);
+            more = moved > 0;
             const unsigned char *next = nullptr;
             unsigned next_seen = 0;
             if (more) {
-                next = record();
-                next_seen = seen_bits();
+                next_seen = seen_bits(w);
+                if constexpr (kTma)
+                    issue(cur ^ 1);  // read by the block before this one: every lane is past it
+                else
+                    next = record();
             }
             if (fresh) {
                 fresh = false;
                 // q as the A operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
                 // words kW t + u, the latter / 16 because their codes are high nibbles
-                const Q *qh = static_cast<const Q *>(p.q) + (size_t(head.b) * p.Hq + head.kvh * G + min(g, G - 1)) * D +
+                const Q *qh = static_cast<const Q *>(p.q) + (size_t(w.heads[sel].b) * p.Hq + w.heads[sel].kvh * G + min(g, G - 1)) * D +
                               t * kW * 8;
                 float x[kW][8], mx = 0.f;
 #pragma unroll
@@ -267,7 +297,6 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
                 }
                 const int e = exponent(mx);
                 const float f = pow2(14 - e), fh = f * 0.0625f;
-                __syncwarp();
 #pragma unroll
                 for (int u = 0; u < kW; ++u) {
                     float a[8];
@@ -275,15 +304,23 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
                     for (int i = 0; i < 8; ++i) a[i] = x[u][i] * (i & 1 ? fh : f);
 #pragma unroll
                     for (int part = 0; part < kQ; ++part)
-                        qa[(u * kQ + part) * 32 + lane] = make_uint4(half_pair(a[0], a[4]), half_pair(a[1], a[5]),
-                                                                     half_pair(a[2], a[6]), half_pair(a[3], a[7]));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qf[part][u][i] = half_pair(a[i], a[i + 4]);
                 }
                 // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)): products' units
                 kq = pow2(e + 10) * p.scale * 1.4426950408889634f;
                 const float toy = pow2(-10 - e);
 #pragma unroll
                 for (int i = 0; i < kG; ++i) qsum[i] *= toy;
-                __syncwarp();
+            }
+            if constexpr (kTma) {
+                if (!mbar_wait(&bars[cur], phase >> cur & 1)) {
+                    failed = true;
+                    break;
+                }
+                phase ^= 1u << cur;
+                load_par(buf + cur * Geom::kBuf, seen);
+                load_k(buf + cur * Geom::kBuf, seen);
             }
 
             // ---- key `lane`'s scales and minima, in fp32, V's scales times the running power of two
@@ -301,7 +338,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
                     lower = f / fscale;
                     fscale = f;
                 }
-                if (more) load_par(next, next_seen);
+                if (!kTma && more) load_par(next, next_seen);
                 // [key]: K's (s, m) per group, then V's; slot rotated by the key's pair against bank conflicts
 #pragma unroll
                 for (int i = 0; i < kG; ++i) {
@@ -335,17 +372,12 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         const uint32_t wd = kc[o][u] >> (8 * s), b0 = wd & kLo, b1 = wd & kHi;
-                        const uint4 qh = qa[(u * kQ) * 32 + lane];
-                        uint32_t a1 = 0, a3 = 0;
-                        if constexpr (kQ == 2) {
-                            const uint4 ql = qa[(u * kQ + 1) * 32 + lane];
-                            a1 = s ? ql.z : ql.x;
-                            a3 = s ? ql.w : ql.y;
-                        }
+                        const uint32_t a0 = qf[0][u][2 * s], a2 = qf[0][u][2 * s + 1];
+                        const uint32_t a1 = kQ == 2 ? qf[kQ - 1][u][2 * s] : 0u, a3 = kQ == 2 ? qf[kQ - 1][u][2 * s + 1] : 0u;
                         if (u < kG && s == 0)
-                            mma_f16_zero(c[u % kG], qh.x, a1, qh.y, a3, b0, b1);
+                            mma_f16_zero(c[u % kG], a0, a1, a2, a3, b0, b1);
                         else
-                            mma_f16(c[u % kG], s ? qh.z : qh.x, a1, s ? qh.w : qh.y, a3, b0, b1);
+                            mma_f16(c[u % kG], a0, a1, a2, a3, b0, b1);
                     }
                 }
 #pragma unroll
@@ -407,7 +439,8 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
                 }
             }
             __syncwarp();  // the parameters are read: the next block's may be written
-            if (more) load_k(next, next_seen);
+            if (!kTma && more) load_k(next, next_seen);
+            if constexpr (kTma) load_v(buf + cur * Geom::kBuf, seen);
 
             // ---- O += (e s) n, tile by tile
             const float2 sco = make_float2(sc * lower, sc * lower);
@@ -438,19 +471,38 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1) kv4_kernel(
                         }
                     }
                 }
-            if (more) load_v(next, next_seen);
+            if (!kTma && more) load_v(next, next_seen);
+            cur ^= 1;
 
-            if (!same) {  // the stretch leaves the head
-                close(head, head.began && last, 2 * warp + (more ? 0 : 1));
+            if (moved != 1) {  // the stretch leaves the head
+                const Head head = w.heads[sel];
+                close(head, head.began && n + 1 == head.nb, 2 * warp + (more ? 0 : 1));
                 reset();
                 fresh = true;
-                head = Owner(w);
+                sel = w.sel;
             }
             seen = next_seen;
         }
+        if (failed) {
+            // SANTA_ERR_TIMEOUT, location code 5; wait, bounded, for the copies in flight
+            if (lane == 0) {
+                raise_flag(p, SANTA_ERR_TIMEOUT | (5u << 8));
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&bars[cur], phase >> cur & 1) && clock64() - t0 < kWaitCycles) {
+                }
+                while (w.left > 0 && !mbar_try_wait(&bars[cur ^ 1], phase >> (cur ^ 1) & 1) &&
+                       clock64() - t0 < kWaitCycles) {
+                }
+            }
+            __syncwarp();
+        }
     }
     join_pieces<NW, D>(
-        sp, sh, [&](int slot) { return const_cast<const float *>(pieces) + size_t(slot) * GT * D; },
+        sp, sh,
+        [&](int slot) {
+            return slot & 1 ? reinterpret_cast<const float *>(smem + (slot >> 1) * Geom::kSlot)
+                            : const_cast<const float *>(first_piece) + size_t(slot >> 1) * GT * D;
+        },
         reinterpret_cast<float *>(smem));  // the pieces are consumed when it is written
 }
 
@@ -462,11 +514,19 @@ cudaError_t launch(const SplitParams &sp, cudaStream_t stream, const Timing &tm)
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int ctas = sms < kSplitCtaBound ? sms : kSplitCtaBound;
+    CUtensorMap map = {};
+    if (Geom::kTma) {  // [rows][Hkv][record], boxes of one head's record x 32 rows
+        const cuuint64_t dims[3] = {cuuint64_t(kv4_record(D)), cuuint64_t(sp.p.Hkv), cuuint64_t(sp.p.total_tokens)};
+        const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+        const cuuint32_t box[3] = {cuuint32_t(kv4_record(D)), 1u, cuuint32_t(kBlock)};
+        if (!cache_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, sp.kv4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorUnknown;
+    }
     auto go = [&](auto kern) {
         cudaError_t r = ensure_smem(kern, Geom::kTotal);
         if (r != cudaSuccess) return r;
         record_event(tm.begin, stream);
-        r = launch_kernel(kern, dim3(unsigned(ctas)), dim3(Geom::kWarps * 32), Geom::kTotal, stream, true, 0, false, sp);
+        r = launch_kernel(kern, dim3(unsigned(ctas)), dim3(Geom::kWarps * 32), Geom::kTotal, stream, true, 0, false, map, sp);
         record_event(tm.end, stream);
         return r;
     };

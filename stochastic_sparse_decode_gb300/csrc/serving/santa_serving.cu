@@ -1,5 +1,7 @@
 // santa_serving.cu -- the C entry points of the operators around the attention:
 // argument checks and launches.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstdint>
 
@@ -128,6 +130,27 @@ int attend(const santa_problem *p, const santa_window *w, const santa_pages *pag
 }
 
 }  // namespace
+
+namespace santa {
+
+bool cache_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, const cuuint64_t (&dims)[3],
+               const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
+                   : nullptr;
+    }();
+    const cuuint32_t step[3] = {1u, 1u, 1u};
+    return encode && encode(map, type, 3, const_cast<void *>(base), dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace santa
 
 extern "C" {
 

@@ -58,6 +58,9 @@ struct SplitParams {
     float *part;               // [CTAs][2][G][D] the unnormalised sums
 };
 constexpr int kSplitCtaBound = 160;  // CTAs of a split launch at most (the workspace is sized for it)
+// A 3-D tensor map (santa_serving.cu); false if the driver refuses it.
+bool cache_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, const cuuint64_t (&dims)[3],
+               const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 cudaError_t launch_window(const SplitParams &p, int dtype, cudaStream_t stream, const Timing &tm);
 cudaError_t launch_kv4(const SplitParams &p, int dtype, cudaStream_t stream, const Timing &tm);
 

@@ -40,6 +40,7 @@ struct Head {
     int start;        // the sequence's first row (contiguous cache; rows fit 31 bits)
     Visible vis;
     int nsb, wb0;     // sink blocks; the window's first block
+    bool began;       // the head begins in the warp's stretch
     __device__ __forceinline__ int first_key(int n) const { return kBlock * (n < nsb ? n : wb0 + n - nsb); }
 };
 __device__ __forceinline__ void set_blocks(Head &h, int L, const SplitParams &sp) {
@@ -86,6 +87,7 @@ struct SplitShared {
     float M[2 * NW][kMaxGroup], Z[2 * NW][kMaxGroup];  // pieces 2w (first head of warp w), 2w + 1 (last)
     long long u0[2 * NW];                              // the piece's head; -1: no piece
     int b[2 * NW], kvh[2 * NW], nb[2 * NW];
+    Head heads[NW][2];                                 // see Walk
     float coef[2 * NW][kMaxGroup];                     // weight of a piece in its head's sum
     int list[2 * NW + 1];                              // the pieces there are, in order
     int begin[2 * NW + 1];                             // where in `list` each head's pieces begin
@@ -99,23 +101,38 @@ struct SplitShared {
     long long scan[NW + 1];
 };
 
-// A warp's place in the walk.
+// A warp's place in the walk.  Its head, and the one before it (which the block being
+// computed may still belong to), lie in shared memory: they are looked at once per run of
+// blocks, and would hold a dozen registers per thread.
 struct Walk {
     int left;     // units of the stretch, this one included
-    int n;        // block of `head`
-    int key0;     // its first key
+    int n, run;   // block of the head; where its run of consecutive keys ends
+    int key0;     // the block's first key
     int in_page;  // paged: where in its page the block begins
     int row;      // its first cache row; -1: a bad page id (flagged), its keys are dropped
-    bool began;   // `head` begins in this stretch
-    Head head;
+    int sel;      // the head: heads[sel]
+    Head *heads;  // [2], the warp's own
 };
 
-// The row of block w.n, by the page table.
+// Makes h the head of `slot`; every lane holds the same h.
+__device__ __forceinline__ void put_head(Walk &w, int slot, const Head &h) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) w.heads[slot] = h;
+    __syncwarp();
+}
+// The run and the row of block w.n of h, by the page table.
 template <bool kPaged>
-__device__ __forceinline__ void place(const SplitParams &sp, Walk &w) {
-    w.key0 = w.head.first_key(w.n);
-    w.row = int(key_row<kPaged>(sp.p, w.head.b, w.head.start, w.key0));
+__device__ __forceinline__ void place(const SplitParams &sp, Walk &w, const Head &h) {
+    w.run = w.n < h.nsb ? h.nsb : h.nb;
+    w.key0 = h.first_key(w.n);
+    w.row = int(key_row<kPaged>(sp.p, h.b, h.start, w.key0));
     if constexpr (kPaged) w.in_page = w.key0 % sp.p.page_size;
+}
+// Which of the 32 keys of the walk's block the query sees, a bit each.
+__device__ __forceinline__ unsigned seen_bits(const Walk &w) {
+    const Visible v = w.heads[w.sel].vis;
+    const int key = w.key0 + (threadIdx.x & 31);
+    return __ballot_sync(kFull, w.row >= 0 && key < v.L && (key < v.s || key >= v.lo));
 }
 
 __device__ __forceinline__ void zero_row(const Params &p, int b) {
@@ -259,63 +276,62 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         w.left = 0;
         return 0;
     }
-    load_head<kPaged>(w.head, sp, b);
+    Head h;
+    load_head<kPaged>(h, sp, b);
     const long long rem = x - prefix * p.Hkv;
-    w.head.kvh = int(divide(rem, w.head.nb));
-    w.n = int(rem - (long long)w.head.kvh * w.head.nb);
-    w.head.u0 = x - w.n;
-    w.began = w.n == 0;
-    place<kPaged>(sp, w);
+    h.kvh = int(divide(rem, h.nb));
+    w.n = int(rem - (long long)h.kvh * h.nb);
+    h.u0 = x - w.n;
+    h.began = w.n == 0;
+    w.sel = 0;
+    w.heads = sh.heads[warp];
+    place<kPaged>(sp, w, h);
+    put_head(w, 0, h);
     return 1;
 }
 
-// Moves to the next unit; false at the stretch's end.
+// Moves to the next unit.  0: the stretch has ended; 1: the next block of the head; 2: of
+// another head (w.sel has changed).
 template <bool kPaged>
-__device__ __forceinline__ bool next_unit(const SplitParams &sp, Walk &w) {
-    if (--w.left <= 0) return false;
-    if (++w.n < w.head.nb) {
-        if (w.n != w.head.nsb) {  // the next block of the sequence
-            w.key0 += kBlock;
-            if constexpr (!kPaged) {
-                w.row += kBlock;
-                return true;
-            } else {
-                w.in_page += kBlock;
-                if (w.in_page < sp.p.page_size) {
-                    if (w.row >= 0) w.row += kBlock;
-                    return true;
-                }
+__device__ __forceinline__ int next_unit(const SplitParams &sp, Walk &w) {
+    if (--w.left <= 0) return 0;
+    if (++w.n < w.run) {
+        w.key0 += kBlock;
+        if constexpr (!kPaged) {
+            w.row += kBlock;
+            return 1;
+        } else {
+            w.in_page += kBlock;
+            if (w.in_page < sp.p.page_size) {
+                if (w.row >= 0) w.row += kBlock;
+                return 1;
             }
         }
-        place<kPaged>(sp, w);
-        return true;
+    }
+    Head h = w.heads[w.sel];
+    if (w.n < h.nb) {  // another page, or from the sinks to the window
+        place<kPaged>(sp, w, h);
+        return 1;
     }
     w.n = 0;
-    w.head.u0 += w.head.nb;
-    w.began = true;
-    if (++w.head.kvh >= sp.p.Hkv) {
-        w.head.kvh = 0;
-        int b = w.head.b;
+    h.u0 += h.nb;
+    h.began = true;
+    if (++h.kvh >= sp.p.Hkv) {
+        h.kvh = 0;
+        int b = h.b;
         do {
-            load_head<kPaged>(w.head, sp, ++b);
-        } while (w.head.nb == 0 && b + 1 < sp.p.B);
+            load_head<kPaged>(h, sp, ++b);
+        } while (h.nb == 0 && b + 1 < sp.p.B);
     }
-    place<kPaged>(sp, w);
-    return true;
+    place<kPaged>(sp, w, h);
+    w.sel ^= 1;
+    put_head(w, w.sel, h);
+    return 2;
 }
-
-// The head that a warp's state belongs to.
-struct Owner {
-    long long u0;
-    int b, kvh, nb;
-    bool began;  // within the stretch
-    __device__ __forceinline__ Owner(const Walk &w)
-        : u0(w.head.u0), b(w.head.b), kvh(w.head.kvh), nb(w.head.nb), began(w.began) {}
-};
 
 // Notes that piece `slot` belongs to `h`.  One lane.
 template <int NW>
-__device__ __forceinline__ void note_piece(SplitShared<NW> &sh, int slot, const Owner &h) {
+__device__ __forceinline__ void note_piece(SplitShared<NW> &sh, int slot, const Head &h) {
     sh.u0[slot] = h.u0;
     sh.b[slot] = h.b;
     sh.kvh[slot] = h.kvh;

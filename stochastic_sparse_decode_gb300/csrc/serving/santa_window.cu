@@ -21,8 +21,6 @@
 // the tensor cores' additions truncate, and a chain over thousands of keys would drift.
 // fp32: a lane forms the whole dot products of one key (rows read along the swizzle
 // without bank conflicts), then owns d / 32 dimensions of the sums.
-#include <cudaTypedefs.h>
-
 #include "santa_split.cuh"
 #include "santa_stream.cuh"
 
@@ -59,7 +57,7 @@ struct WindowGeom {
     static constexpr size_t kEs = kFirst + size_t(kWarps) * GT * D * 4;
     static constexpr size_t kBars = kEs + (sizeof(T) == 4 ? size_t(kWarps) * 32 * GT * 4 : 0);
     static constexpr size_t kShared = (kBars + size_t(kWarps) * 2 * 8 + 15) & ~size_t(15);
-    static constexpr size_t kTotal = 1024 + kShared + sizeof(SplitShared<kWarps>);
+    static constexpr size_t kTotal = kShared + sizeof(SplitShared<kWarps>);
     static_assert(kTotal <= 227 * 1024, "shared memory");
     // after the walk the buffers hold a warp's last piece; the joined heads' coefficients
     // and partial sums take the room of the first pieces and of other buffers
@@ -79,8 +77,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = p.G;
 
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = align1024(smem_raw);
+    extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *kbuf = smem + size_t(warp) * 2 * WG::kBytes, *vbuf = kbuf + WG::kBytes;
     float *first_piece = reinterpret_cast<float *>(smem + WG::kFirst);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + WG::kBars) + warp * 2;
@@ -137,7 +134,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
             for (int e = 0; e < kE; ++e) O[h][e] = 0.f;
     };
     // Closes the state for `head`: final outputs (kind 0), or piece `slot` with its sums at o.
-    auto close = [&](const Owner &head, bool final, int slot, float *o) {
+    auto close = [&](const Head &head, bool final, int slot, float *o) {
         if constexpr (kMma) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -181,24 +178,24 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
     const float scale2 = p.scale * 1.4426950408889634f;  // logits in base 2
     bool failed = false, k_flying = true;  // k_flying: the K barrier's phase is still to complete
     if (any > 0) {
-        Owner head(w);  // of the block being computed; w runs one block ahead
-        Visible vis = w.head.vis;
-        int key0 = w.key0;
+        int sel = w.sel;  // the head of the block being computed; w runs one block ahead
+        unsigned seen = seen_bits(w);  // keys of the block that the query sees
         int row = w.row;
-        issue(0, row, head.kvh);
-        issue(1, row, head.kvh);
+        issue(0, row, w.heads[sel].kvh);
+        issue(1, row, w.heads[sel].kvh);
         uint32_t qf[kMma ? D / 16 : 1][2];
         uint32_t phK = 0, phV = 0;
         bool fresh = true;  // the state is empty and q not loaded
         reset();
         for (bool more = true; more;) {
-            const bool last = w.n + 1 == head.nb;  // the block is its head's last
-            more = next_unit<kPaged>(sp, w);
-            const bool same = more && w.head.u0 == head.u0;
+            const int n = w.n, moved = next_unit<kPaged>(sp, w);
+            more = moved > 0;
+            const unsigned next_seen = more ? seen_bits(w) : 0u;
+            const int b = w.heads[sel].b, kvh = w.heads[sel].kvh;
             if (fresh && kMma) {
                 // lane (g, t): dimensions 16 ks + 2t, +1 and 16 ks + 2t + 8, +9 of head g
                 const uint32_t *qh = reinterpret_cast<const uint32_t *>(
-                    static_cast<const uint16_t *>(p.q) + (size_t(head.b) * p.Hq + head.kvh * G + min(g, G - 1)) * D);
+                    static_cast<const uint16_t *>(p.q) + (size_t(b) * p.Hq + kvh * G + min(g, G - 1)) * D);
 #pragma unroll
                 for (int ks = 0; ks < (kMma ? D / 16 : 1); ++ks) {
                     qf[ks][0] = g < G ? __ldg(qh + 8 * ks + t) : 0u;
@@ -206,10 +203,6 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                 }
             }
             fresh = false;
-            auto seen = [&](int r) {
-                const int key = key0 + r;
-                return key < vis.L && (key < vis.s || key >= vis.lo);
-            };
             if (!mbar_wait(&bars[0], phK)) {
                 failed = true;
                 break;
@@ -221,7 +214,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                 if constexpr (kMma) {
                     chunk_logits_mma<D>(kbuf, qf, lane, c);
                 } else {
-                    const float *qh = static_cast<const float *>(p.q) + (size_t(head.b) * p.Hq + head.kvh * G) * D;
+                    const float *qh = static_cast<const float *>(p.q) + (size_t(b) * p.Hq + kvh * G) * D;
                     float2 acc[GT];
 #pragma unroll
                     for (int h = 0; h < GT; ++h) acc[h] = make_float2(0.f, 0.f);
@@ -241,7 +234,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                 }
             }
             __syncwarp();
-            if (more) issue(0, w.row, w.head.kvh);  // the K buffer is free
+            if (more) issue(0, w.row, w.heads[w.sel].kvh);  // the K buffer is free
             k_flying = more;
 
             uint32_t pf[3][4];  // weights, part by part: keys 8 o + 2t, + 1 of head g
@@ -251,7 +244,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                     float xv[2][4];
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
-                        const bool in = seen(8 * o + g);
+                        const bool in = seen >> (8 * o + g) & 1;
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             xv[j][o] = in ? c[o >> 1][(o & 1) * 2 + j] * scale2 : -INFINITY;
@@ -283,7 +276,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                     }
                 } else {
                     float *es = reinterpret_cast<float *>(smem + WG::kEs) + warp * 32 * GT;
-                    const bool in = seen(lane);
+                    const bool in = seen >> lane & 1;
 #pragma unroll
                     for (int h = 0; h < GT; ++h) {
                         const float xh = in ? x[h] * scale2 : -INFINITY;
@@ -303,12 +296,10 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
             }
             phV ^= 1u;
             if (row >= 0) {
-                const bool partial = key0 + kBlock > vis.L ||
-                                     (key0 < vis.lo && key0 + kBlock > vis.s);
-                if (partial) {  // rows that the query must not see: zeros
+                if (seen != kFull) {  // rows that the query must not see: zeros
                     for (int i = lane; i < kBlock * Geo::kBoxes * 8; i += 32) {
                         const int r = (i >> 3) % kBlock, bx = (i >> 3) / kBlock;
-                        if (!seen(r))
+                        if (!(seen >> r & 1))
                             *reinterpret_cast<uint4 *>(vbuf + bx * kChunkBoxBytes + r * 128 + (i & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                     }
@@ -364,10 +355,11 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                 }
             }
             __syncwarp();
-            if (more) issue(1, w.row, w.head.kvh);  // the V buffer is free
+            if (more) issue(1, w.row, w.heads[w.sel].kvh);  // the V buffer is free
 
-            if (!same) {  // the stretch leaves the head
-                if (head.began && last)
+            if (moved != 1) {  // the stretch leaves the head
+                const Head head = w.heads[sel];
+                if (head.began && n + 1 == head.nb)
                     close(head, true, 0, nullptr);
                 else if (more)
                     close(head, false, 2 * warp, first_piece + size_t(warp) * GT * D);
@@ -375,10 +367,9 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                     close(head, false, 2 * warp + 1, reinterpret_cast<float *>(kbuf));
                 reset();
                 fresh = true;
-                head = Owner(w);
-                vis = w.head.vis;
+                sel = w.sel;
             }
-            key0 = w.key0;
+            seen = next_seen;
             row = w.row;
         }
         if (failed) {
@@ -406,30 +397,19 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
 }
 
 // Tensor map of a [rows][Hkv][d] cache: boxes of 128 bytes of one head's row x 32 rows.
-bool cache_map(CUtensorMap *map, const void *base, int dtype, const Params &p) {
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
-        return e == cudaSuccess && q == cudaDriverEntryPointSuccess
-                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
-                   : nullptr;
-    }();
-    if (!encode) return false;
+bool kv_map(CUtensorMap *map, const void *base, int dtype, const Params &p) {
     const int es = dtype == SANTA_BF16 ? 2 : 4;
     const cuuint64_t dims[3] = {cuuint64_t(p.D), cuuint64_t(p.Hkv), cuuint64_t(p.total_tokens)};
     const cuuint64_t strides[2] = {cuuint64_t(p.D) * es, cuuint64_t(p.Hkv) * p.D * es};
-    const cuuint32_t box[3] = {cuuint32_t(128 / es), 1u, cuuint32_t(kBlock)}, step[3] = {1u, 1u, 1u};
-    return encode(map, dtype == SANTA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-                  const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {cuuint32_t(128 / es), 1u, cuuint32_t(kBlock)};
+    return cache_map(map, dtype == SANTA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base,
+                     dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <typename T, int D, int GT>
 cudaError_t launch(const SplitParams &sp, int dtype, cudaStream_t stream, const Timing &tm) {
     CUtensorMap kmap, vmap;
-    if (!cache_map(&kmap, sp.p.k, dtype, sp.p) || !cache_map(&vmap, sp.p.v, dtype, sp.p)) return cudaErrorUnknown;
+    if (!kv_map(&kmap, sp.p.k, dtype, sp.p) || !kv_map(&vmap, sp.p.v, dtype, sp.p)) return cudaErrorUnknown;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
