@@ -8,22 +8,26 @@
 // they lie in memory.  A code needs no conversion: masked out of its word it is, as an fp16
 // bit pattern, the subnormal n 2^-24 (low nibble of a byte) or n 2^-20 (high nibble), which
 // the tensor cores multiply exactly; the powers of two go into q and the final factor.
-// Queries and weights are the A operand (rows = heads), codes the B operand, so the logits
-// come out in the layout in which the weights go in, and a lane deals with one head.  A word
-// of K's codes is the B operand of two products (4 ands, 1 shift); two keys' words of V,
-// paired by byte permutes, those of eight (2 permutes, 8 ands, 2 shifts).  The rows' scales and
-// minima are converted once, by the lane that has the key, and shared through shared memory.
-// d = 128: a warp's blocks come by TMA (boxes of 32 records) into two buffers of its own.
-// d = 64: a record is 72 bytes, which TMA's strides cannot express; the codes go from global
-// memory to registers, the next block's while the current one is computed.
+// Codes are the A operand of both (rows: keys, then elements), queries and weights the B
+// operand (columns: heads).  A word of K's codes gives a lane the A fragments of two products
+// (4 ands, 1 shift); two keys' words of V, paired by byte permutes, those of eight (2
+// permutes, 8 ands, 2 shifts).  The weights turn from the layout in which the logits come out
+// into the one in which they go in by movmatrix.
 //
 // Precision: q is scaled by a power of two per head to fit fp16 (a bf16 q is exact so; an
-// fp32 q is taken in two parts, 22 bits, the second in the A operand's rows 8 .. 15); the
-// weights e_j s_jg likewise in two parts, rows 0 .. 7 and 8 .. 15 of one product, under a
-// running power of two that keeps the largest scale of the row's values in range.
+// fp32 q is taken in two parts, 22 bits); the weights e_j s_jg likewise in two parts, under a
+// running power of two that keeps the largest scale of the row's values in range.  With at
+// most four heads the eight columns hold the heads twice: the logits of the copies cost
+// nothing, and the copies' weights are the second parts, so one product takes both.
 // Everything else is fp32.  The online softmax and the sharing out of the keys are those of
 // the windowed kernel (santa_split.cuh): each block's sums start from zero and join O by an
 // fp32 fma.
+//
+// The rows' scales and minima are converted once, by the lane that has the key, and shared
+// through shared memory, each twice in a row for packed fp32 arithmetic on pairs of heads.
+// d = 128: a warp's blocks come by TMA (boxes of 32 records) into two buffers of its own.
+// d = 64: a record is 72 bytes, which TMA's strides cannot express; the codes go from global
+// memory to registers, the next block's while the current one is computed.
 #include <cuda_fp16.h>
 
 #include "santa_split.cuh"
@@ -33,7 +37,6 @@ namespace santa {
 
 namespace {
 
-// d = A B (+ d): A's rows 0 .. 7 are (a0, a2), rows 8 .. 15 (a1, a3).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm(
@@ -42,6 +45,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same on a zero accumulator.
 __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
     asm(
@@ -49,6 +53,11 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
         "{%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 // (x, y) as an fp16 pair; x and y become what the rounding left.
 __device__ __forceinline__ uint32_t half_pair(float &x, float &y) {
@@ -74,9 +83,10 @@ struct Kv4Geom {
     static constexpr bool kTma = D == 128;
     static constexpr int kQ = sizeof(Q) == 2 ? 1 : 2;        // fp16 parts of q
     static constexpr int kWarps = kTma && (GT > 4 || kQ > 1) ? 12 : 16;
+    static constexpr bool kTwice = GT <= 4;                  // the columns hold the heads twice
     static constexpr int kG = D / 64;
     static constexpr int kBuf = kTma ? kBlock * kv4_record(D) : 0;  // bytes of a block
-    static constexpr int kParBytes = kBlock * kG * 16;       // its (scale, minimum) of K and of V in fp32
+    static constexpr int kParBytes = kBlock * kG * 32;       // its scales and minima of K and of V, each twice, fp32
     static constexpr size_t kPiece = size_t(GT) * D * 4;
     // shared memory: two buffers per warp (its last piece when the walk is over; d = 64: that piece
     // alone), first pieces, parameters, mbarriers, shared state
@@ -98,7 +108,9 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
     constexpr int NW = Geom::kWarps, kG = Geom::kG, kQ = Geom::kQ;
     constexpr bool kTma = Geom::kTma;
     constexpr int kW = D / 32;   // words of K's codes per key and lane; V: kW / 2
-    constexpr int kTiles = D / 8;
+    constexpr int kTiles = D / 16;
+    constexpr bool kTwice = Geom::kTwice;
+    constexpr int kParts = kTwice ? 1 : 2;  // products that take the weights' parts
     constexpr int kRec = kv4_record(D);
     const Params &p = sp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -186,46 +198,53 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
         }
     };
 
-    // State of head g: M, the shares of the lane's own keys of Z and of the sums e_j m_jg, and
-    // O: tile n (a nibble of the lane's V words) holds columns 2t, 2t + 1, that is element n of
-    // words kW / 2 (2t) .. and kW / 2 (2t + 1) .., times fscale 2^-24 (n even) or 2^-20.
-    float M, Z, base[kG], O[kTiles][2], fscale;
+    // State of the heads of columns 2t, 2t + 1: M, the shares of the lane's own keys of Z and of
+    // the sums of e_j m_jg, and O^T: tile (word i of the lane's V words, q) holds elements 2q
+    // (O[..][0 .. 1]) and 2q + 1 (O[..][2 .. 3]) of word (kW / 2) g + i, times fscale 2^-24 and 2^-20.
+    const int h0 = kTwice ? 2 * (t & 1) : 2 * t;  // head of column 2t
+    float M[2], Z[2], base[kG][2], O[kTiles][4], fscale;
     auto reset = [&]() {
-        M = -INFINITY;
-        Z = 0.f;
+        M[0] = M[1] = -INFINITY;
+        Z[0] = Z[1] = 0.f;
         fscale = pow2(60);  // larger than any block allows
 #pragma unroll
-        for (int i = 0; i < kG; ++i) base[i] = 0.f;
+        for (int i = 0; i < kG; ++i) base[i][0] = base[i][1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) O[n][0] = O[n][1] = 0.f;
+        for (int n = 0; n < kTiles; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
     };
     auto close = [&](const Head &head, bool final, int slot) {
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-            Z += __shfl_xor_sync(kFull, Z, x);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < kG; ++i) base[i] += __shfl_xor_sync(kFull, base[i], x);
+            for (int x = 4; x < 32; x <<= 1) {
+                Z[j] += __shfl_xor_sync(kFull, Z[j], x);
+#pragma unroll
+                for (int i = 0; i < kG; ++i) base[i][j] += __shfl_xor_sync(kFull, base[i][j], x);
+            }
+        if constexpr (kTwice) {  // the two parts' sums
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) O[n][j] += __shfl_xor_sync(kFull, O[n][j], 2);
         }
-        if (g < G) {
-            float *dst = final ? p.out + (size_t(head.b) * p.Hq + head.kvh * G + g) * D
-                               : (slot & 1 ? reinterpret_cast<float *>(buf) : first_piece + size_t(warp) * GT * D) + g * D;
-            const float inv = !final ? 1.f : Z == 0.f ? 0.f : 1.f / Z;
-            const float f[2] = {16777216.f / fscale, 1048576.f / fscale};  // powers of two
+        const float f0 = 16777216.f / fscale, f1 = 1048576.f / fscale;  // powers of two
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+        for (int j = 0; j < 2; ++j) {
+            const int h = h0 + j;
+            if (h < G && (!kTwice || t < 2)) {
+                float *dst = final ? p.out + (size_t(head.b) * p.Hq + head.kvh * G + h) * D
+                                   : (slot & 1 ? reinterpret_cast<float *>(buf) : first_piece + size_t(warp) * GT * D) + h * D;
+                const float inv = !final ? 1.f : Z[j] == 0.f ? 0.f : 1.f / Z[j];
 #pragma unroll
-                for (int n = 0; n < kTiles; n += 4) {
-                    float4 o;
-                    const float b = base[n / 8 % kG];
-                    o.x = fmaf(O[n][c], f[0], b) * inv;
-                    o.y = fmaf(O[n + 1][c], f[1], b) * inv;
-                    o.z = fmaf(O[n + 2][c], f[0], b) * inv;
-                    o.w = fmaf(O[n + 3][c], f[1], b) * inv;
-                    *reinterpret_cast<float4 *>(dst + (2 * t + c) * kTiles + n) = o;
+                for (int n = 0; n < kTiles; ++n) {
+                    const int i = n / 4, at = 8 * (kW / 2 * g + i) + 2 * (n % 4);
+                    *reinterpret_cast<float2 *>(dst + at) = make_float2(fmaf(O[n][j], f0, base[i % kG][j]) * inv,
+                                                                        fmaf(O[n][2 + j], f1, base[i % kG][j]) * inv);
                 }
-            if (!final && t == 0) {
-                sh.M[slot][g] = M;
-                sh.Z[slot][g] = Z;
+                if (!final && g == 0) {
+                    sh.M[slot][h] = M[j];
+                    sh.Z[slot][h] = Z[j];
+                }
             }
         }
         if (!final && lane == 0) note_piece(sh, slot, head);
@@ -242,10 +261,11 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             load_k(rec, seen);
             load_v(rec, seen);
         }
-        uint32_t qf[kQ][kW][4];  // the A operand of q, see below
+        uint32_t qf[kQ][kW][4];  // the B operand of q, see below
         int cur = 0;             // the buffer of the block
         uint32_t phase = 0;
-        float qsum[kG], kq = 0.f;  // of head g: sum(q_g) and the logits' factor: x = kq y, base 2
+        float2 qsum[kG], kq;     // of the columns' heads: sum(q_g) and the logits' factor: x = kq y, base 2
+        const float part2 = kTwice && t >= 2 ? 1.f : 0.f;
         bool fresh = true, failed = false;
         reset();
         for (bool more = true; more;) {
@@ -262,13 +282,14 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             }
             if (fresh) {
                 fresh = false;
-                // q as the A operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
-                // words kW t + u, the latter / 16 because their codes are high nibbles
-                const Q *qh = static_cast<const Q *>(p.q) + (size_t(w.heads[sel].b) * p.Hq + w.heads[sel].kvh * G + min(g, G - 1)) * D +
-                              t * kW * 8;
-                float x[kW][8], mx = 0.f;
+                // q as the B operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
+                // words kW t + u of the head of column g, the latter / 16 because their codes are high nibbles
+                const int hg = kTwice ? g & 3 : g;
+                const Q *qh = static_cast<const Q *>(p.q) +
+                              (size_t(w.heads[sel].b) * p.Hq + w.heads[sel].kvh * G + min(hg, G - 1)) * D + t * kW * 8;
+                float x[kW][8], mx = 0.f, sum[kG];
 #pragma unroll
-                for (int i = 0; i < kG; ++i) qsum[i] = 0.f;
+                for (int i = 0; i < kG; ++i) sum[i] = 0.f;
 #pragma unroll
                 for (int u = 0; u < kW; ++u) {
                     constexpr int kVec = 8 * sizeof(Q) / 16;
@@ -284,16 +305,16 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if (g >= G) x[u][i] = 0.f;
+                        if (hg >= G) x[u][i] = 0.f;
                         mx = fmaxf(mx, fabsf(x[u][i]));
-                        qsum[u % kG] += x[u][i];
+                        sum[u % kG] += x[u][i];
                     }
                 }
 #pragma unroll
                 for (int s = 1; s < 4; s <<= 1) {
                     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, s));
 #pragma unroll
-                    for (int i = 0; i < kG; ++i) qsum[i] += __shfl_xor_sync(kFull, qsum[i], s);
+                    for (int i = 0; i < kG; ++i) sum[i] += __shfl_xor_sync(kFull, sum[i], s);
                 }
                 const int e = exponent(mx);
                 const float f = pow2(14 - e), fh = f * 0.0625f;
@@ -307,11 +328,14 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) qf[part][u][i] = half_pair(a[i], a[i + 4]);
                 }
-                // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)): products' units
-                kq = pow2(e + 10) * p.scale * 1.4426950408889634f;
-                const float toy = pow2(-10 - e);
+                // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)), in the products' units
+                const int e0 = __shfl_sync(kFull, e, 4 * h0), e1 = __shfl_sync(kFull, e, 4 * (h0 + 1));
+                const float scale2 = p.scale * 1.4426950408889634f;
+                kq = make_float2(pow2(e0 + 10) * scale2, pow2(e1 + 10) * scale2);
 #pragma unroll
-                for (int i = 0; i < kG; ++i) qsum[i] *= toy;
+                for (int i = 0; i < kG; ++i)
+                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(-10 - e0),
+                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(-10 - e1));
             }
             if constexpr (kTma) {
                 if (!mbar_wait(&bars[cur], phase >> cur & 1)) {
@@ -339,111 +363,117 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     fscale = f;
                 }
                 if (!kTma && more) load_par(next, next_seen);
-                // [key]: K's (s, m) per group, then V's; slot rotated by the key's pair against bank conflicts
+                // per key and group (s, s, m, m) of K, then of V; the slots of a key turn with the key
+                // against bank conflicts
 #pragma unroll
-                for (int i = 0; i < kG; ++i) {
-                    if constexpr (kG == 2) {
-                        const float2 a = sm[2 * i], b = sm[2 * i + 1];
-                        par[lane * 2 + (i ^ (lane >> 2 & 1))] = i == 0 ? make_float4(a.x, a.y, b.x, b.y)
-                                                                      : make_float4(a.x * fscale, a.y, b.x * fscale, b.y);
-                    } else {
-                        par[lane] = make_float4(sm[0].x, sm[0].y, sm[1].x * fscale, sm[1].y);
-                    }
+                for (int i = 0; i < 2 * kG; ++i) {
+                    const float sc = i < kG ? sm[i].x : sm[i].x * fscale;
+                    par[lane * 2 * kG + ((i + lane) & (2 * kG - 1))] = make_float4(sc, sc, sm[i].y, sm[i].y);
                 }
                 __syncwarp();
             }
-            // (scale, minimum) per group of K (which = 0) or V (1) of key r
-            auto params = [&](int which, int r) -> float4 {
-                if constexpr (kG == 2) {
-                    return par[r * 2 + (which ^ (r >> 2 & 1))];
-                } else {
-                    const float2 x = reinterpret_cast<const float2 *>(par + r)[which];
-                    return make_float4(x.x, x.y, 0.f, 0.f);
-                }
+            auto params = [&](int i, int r, float2 &sc, float2 &mn) {  // i: group of K, kG + group of V
+                const float4 v = par[r * 2 * kG + ((i + r) & (2 * kG - 1))];
+                sc = make_float2(v.x, v.y);
+                mn = make_float2(v.z, v.w);
             };
 
-            // ---- logits of head g and keys 8 o + 2t + i
-            float y[4][2];
+            // ---- logits of the columns' heads and keys 8 o + g
+            float2 y[4];
 #pragma unroll
-            for (int o = 0; o < 4; ++o) {
+            for (int mt = 0; mt < 2; ++mt) {
                 float c[kG][4];
 #pragma unroll
-                for (int u = 0; u < kW; ++u) {
+                for (int u = 0; u < kW; ++u)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint32_t wd = kc[o][u] >> (8 * s), b0 = wd & kLo, b1 = wd & kHi;
-                        const uint32_t a0 = qf[0][u][2 * s], a2 = qf[0][u][2 * s + 1];
-                        const uint32_t a1 = kQ == 2 ? qf[kQ - 1][u][2 * s] : 0u, a3 = kQ == 2 ? qf[kQ - 1][u][2 * s + 1] : 0u;
-                        if (u < kG && s == 0)
-                            mma_f16_zero(c[u % kG], a0, a1, a2, a3, b0, b1);
-                        else
-                            mma_f16(c[u % kG], a0, a1, a2, a3, b0, b1);
-                    }
-                }
+                        const uint32_t a = kc[2 * mt][u] >> (8 * s), b = kc[2 * mt + 1][u] >> (8 * s);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 sm = params(0, 8 * o + 2 * t + i);
-                    const float c0 = kQ == 2 ? c[0][i] + c[0][2 + i] : c[0][i];
-                    y[o][i] = fmaf(sm.x, c0, sm.y * qsum[0]);
+                        for (int part = kQ - 1; part >= 0; --part) {
+                            if (u < kG && s == 0 && part == kQ - 1)
+                                mma_f16_zero(c[u % kG], a & kLo, b & kLo, a & kHi, b & kHi, qf[part][u][2 * s],
+                                             qf[part][u][2 * s + 1]);
+                            else
+                                mma_f16(c[u % kG], a & kLo, b & kLo, a & kHi, b & kHi, qf[part][u][2 * s],
+                                        qf[part][u][2 * s + 1]);
+                        }
+                    }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int o = 2 * mt + hf;
+                    float2 sc, mn;
+                    params(0, 8 * o + g, sc, mn);
+                    y[o] = __ffma2_rn(sc, make_float2(c[0][2 * hf], c[0][2 * hf + 1]), __fmul2_rn(mn, qsum[0]));
                     if constexpr (kG == 2) {
-                        const float c1 = kQ == 2 ? c[1][i] + c[1][2 + i] : c[1][i];
-                        y[o][i] = fmaf(sm.z, c1, fmaf(sm.w, qsum[1], y[o][i]));
+                        params(1, 8 * o + g, sc, mn);
+                        y[o] = __ffma2_rn(mn, qsum[1], y[o]);
+                        y[o] = __ffma2_rn(sc, make_float2(c[1][2 * hf], c[1][2 * hf + 1]), y[o]);
                     }
                 }
             }
+
             // ---- online softmax
             if (seen != kFull) {
 #pragma unroll
                 for (int o = 0; o < 4; ++o)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (!(seen >> (8 * o + 2 * t + i) & 1)) y[o][i] = -INFINITY;
+                    if (!(seen >> (8 * o + g) & 1)) y[o] = make_float2(-INFINITY, -INFINITY);
             }
-            float sc;
+            float2 sc;
             {
-                float m = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1])),
-                                fmaxf(fmaxf(y[2][0], y[2][1]), fmaxf(y[3][0], y[3][1])));
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-                m = fmaxf(M, m * kq);
-                const float ref = m == -INFINITY ? 0.f : m;
-                sc = ex2(M - ref);
-                M = m;
-                float z = 0.f;
+                float m0 = fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x));
+                float m1 = fmaxf(fmaxf(y[0].y, y[1].y), fmaxf(y[2].y, y[3].y));
 #pragma unroll
-                for (int o = 0; o < 4; ++o)
+                for (int x = 4; x < 32; x <<= 1) {
+                    m0 = fmaxf(m0, __shfl_xor_sync(kFull, m0, x));
+                    m1 = fmaxf(m1, __shfl_xor_sync(kFull, m1, x));
+                }
+                m0 = fmaxf(M[0], m0 * kq.x);
+                m1 = fmaxf(M[1], m1 * kq.y);
+                const float2 ref = make_float2(m0 == -INFINITY ? 0.f : -m0, m1 == -INFINITY ? 0.f : -m1);
+                sc = make_float2(ex2(M[0] + ref.x), ex2(M[1] + ref.y));
+                M[0] = m0;
+                M[1] = m1;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        y[o][i] = ex2(fmaf(y[o][i], kq, -ref));
-                        z += y[o][i];
-                    }
-                Z = fmaf(Z, sc, z);
+                for (int o = 0; o < 4; ++o) {
+                    y[o] = __ffma2_rn(y[o], kq, ref);
+                    y[o] = make_float2(ex2(y[o].x), ex2(y[o].y));
+                }
+                const float2 z = __fadd2_rn(__fadd2_rn(y[0], y[1]), __fadd2_rn(y[2], y[3]));
+                const float2 zz = __ffma2_rn(make_float2(Z[0], Z[1]), sc, z);
+                Z[0] = zz.x;
+                Z[1] = zz.y;
             }
 
-            // ---- the weights times V's scales: A operand, rows 0 .. 7 and (what fp16 left) 8 .. 15
-            uint32_t pa[kG][4][2];  // [group][octet][part]
+            // ---- the weights times V's scales, as the B operand
+            uint32_t pf[kG][kParts][4];  // [group][part][octet]
 #pragma unroll
-            for (int i = 0; i < kG; ++i) base[i] *= sc;
+            for (int i = 0; i < kG; ++i) {
+                float2 bs = __fmul2_rn(make_float2(base[i][0], base[i][1]), sc);
 #pragma unroll
-            for (int o = 0; o < 4; ++o) {
-                const float4 u = params(1, 8 * o + 2 * t), v = params(1, 8 * o + 2 * t + 1);
-                base[0] = fmaf(y[o][0], u.y, fmaf(y[o][1], v.y, base[0]));
-                float a = y[o][0] * u.x, b = y[o][1] * v.x;
-                pa[0][o][0] = half_pair(a, b);
-                pa[0][o][1] = half_pair(a, b);
-                if constexpr (kG == 2) {
-                    base[1] = fmaf(y[o][0], u.w, fmaf(y[o][1], v.w, base[1]));
-                    a = y[o][0] * u.z, b = y[o][1] * v.z;
-                    pa[1][o][0] = half_pair(a, b);
-                    pa[1][o][1] = half_pair(a, b);
+                for (int o = 0; o < 4; ++o) {
+                    float2 s, mn;
+                    params(kG + i, 8 * o + g, s, mn);
+                    bs = __ffma2_rn(y[o], mn, bs);
+                    const float2 v = __fmul2_rn(y[o], s);
+                    const __half2 h = __floats2half2_rn(v.x, v.y);
+                    if constexpr (kTwice) {  // first parts in columns 0 .. 3, what they leave in 4 .. 7
+                        const __half2 l = __floats2half2_rn(fmaf(-part2, __low2float(h), v.x), fmaf(-part2, __high2float(h), v.y));
+                        pf[i][0][o] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&l));
+                    } else {
+                        const __half2 l = __floats2half2_rn(v.x - __low2float(h), v.y - __high2float(h));
+                        pf[i][0][o] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&h));
+                        pf[i][kParts - 1][o] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&l));
+                    }
                 }
+                base[i][0] = bs.x;
+                base[i][1] = bs.y;
             }
             __syncwarp();  // the parameters are read: the next block's may be written
             if (!kTma && more) load_k(next, next_seen);
             if constexpr (kTma) load_v(buf + cur * Geom::kBuf, seen);
 
             // ---- O += (e s) n, tile by tile
-            const float2 sco = make_float2(sc * lower, sc * lower);
+            const float2 sco = make_float2(sc.x * lower, sc.y * lower);
 #pragma unroll
             for (int i = 0; i < kW / 2; ++i)
 #pragma unroll
@@ -456,19 +486,22 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                         if (s)
 #pragma unroll
                             for (int o = 0; o < 4; ++o) pr[o] >>= 8;
+                        float acc[4];
 #pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            const uint32_t mask = hi ? kHi : kLo;
-                            const uint32_t(&a)[4][2] = pa[i % kG];
-                            float acc[4];
-                            mma_f16_zero(acc, a[0][0], a[0][1], a[1][0], a[1][1], pr[0] & mask, pr[1] & mask);
-                            mma_f16(acc, a[2][0], a[2][1], a[3][0], a[3][1], pr[2] & mask, pr[3] & mask);
-                            float(&o)[2] = O[8 * i + 4 * half + 2 * s + hi];
-                            const float2 sum = __fadd2_rn(make_float2(acc[0], acc[1]), make_float2(acc[2], acc[3]));
-                            const float2 r = __ffma2_rn(make_float2(o[0], o[1]), sco, sum);
-                            o[0] = r.x;
-                            o[1] = r.y;
-                        }
+                        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                            for (int part = kParts - 1; part >= 0; --part) {
+                                const uint32_t(&b)[4] = pf[i % kG][part];
+                                const uint32_t a = pr[2 * ks], c = pr[2 * ks + 1];
+                                if (ks == 0 && part == kParts - 1)
+                                    mma_f16_zero(acc, a & kLo, a & kHi, c & kLo, c & kHi, b[2 * ks], b[2 * ks + 1]);
+                                else
+                                    mma_f16(acc, a & kLo, a & kHi, c & kLo, c & kHi, b[2 * ks], b[2 * ks + 1]);
+                            }
+                        float(&o)[4] = O[4 * i + 2 * half + s];
+                        const float2 lo = __ffma2_rn(make_float2(o[0], o[1]), sco, make_float2(acc[0], acc[1]));
+                        const float2 hi = __ffma2_rn(make_float2(o[2], o[3]), sco, make_float2(acc[2], acc[3]));
+                        o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
                     }
                 }
             if (!kTma && more) load_v(next, next_seen);
