@@ -11,12 +11,32 @@ to inspect tile records, budgets and sampled indices.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
-from . import (BF16, MODES, Debug, Rope, Window, decode, k_feature_blocked_size, kv4_size, make_pages, make_problem,
-               santa_decode_kv4, santa_decode_prop_bernoulli, santa_decode_prop_paged, santa_decode_window,
-               santa_k_feature_blocked, santa_kv4_append, santa_kv4_read, santa_norm_rope, santa_page_plan,
+from . import (BF16, MODES, Debug, Pages, Rope, Window, _check, _stream, decode, k_feature_blocked_size, kv4_size, lib,
+               make_pages, make_problem, santa_decode_prop_bernoulli, santa_decode_prop_paged, santa_k_feature_blocked,
                santa_prop_pass1, santa_prop_pass2, split_workspace_size, workspace_size)
+
+_F32, _I32, _I64, _U8 = (frozenset((t,)) for t in (torch.float32, torch.int32, torch.int64, torch.uint8))
+
+# torch's own shortcuts to the current device and its current stream's handle, where it has them
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _fits(t, dtypes, shape, dev) -> bool:
+    return t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
+def _rows_fit(t) -> bool:
+    """A [tokens][heads][d] tensor whose rows of heads x d elements are whole; tokens may lie apart."""
+    if t.is_contiguous():
+        return True
+    s, n = t.stride(), t.shape
+    return s[2] == 1 and (n[1] == 1 or s[1] == n[2]) and (n[0] == 1 or s[0] >= n[1] * n[2])
 
 
 def rope_table(max_pos, rot_dim, theta=10000.0, device="cuda") -> torch.Tensor:
@@ -36,6 +56,7 @@ class Decoder:
         self.device = torch.device(device if device is not None else "cuda")
         self.Tmax = -(-max_len // tile) if max_len > 0 else 0
         self._ws = {}
+        self._prepare()
 
     def workspace(self, mode: str) -> torch.Tensor:
         if mode not in self._ws:
@@ -122,30 +143,44 @@ class Decoder:
         return out
 
     # ---- the operators around the attention
+    #
+    # These calls are a few microseconds of GPU time, so the host's share is kept small: every
+    # tensor is checked by one expression (_fits), and only a refusal looks for the reason.
 
-    def _dtypes(self):
+    def _prepare(self):
+        p = self.problem
         # bf16 may come as its bit pattern, as for the other modes
-        return (torch.bfloat16, torch.int16, torch.uint16) if self.problem.dtype == BF16 else (torch.float32,)
+        self._dt = frozenset((torch.bfloat16, torch.int16, torch.uint16) if p.dtype == BF16 else (torch.float32,))
+        self._q_shape = (p.batch, p.num_q_heads, p.head_dim)
+        self._kv_shape = (p.total_tokens, p.num_kv_heads, p.head_dim)
+        self._kv4_shape = (p.total_tokens, p.num_kv_heads, p.head_dim + p.head_dim // 8)
+        self._pref = ctypes.byref(p)
+        self._windows = {}
 
-    def _tensor(self, name, t, dtypes, *shape, rows=False, like=None):
-        """Refuses a tensor that the C call would misread: dtype, shape (None: any size), layout
+    def _refuse(self, name, t, dtypes, shape, dev, rows=False):
+        """Says why a tensor that the C call would misread is refused: dtype, shape (None: any size), layout
         (`rows`: [tokens][heads][d] whose tokens may lie apart), device."""
         if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-            raise ValueError(f"{name}: a tensor of {' or '.join(map(str, dtypes))} is needed")
+            raise ValueError(f"{name}: a tensor of {' or '.join(sorted(map(str, dtypes)))} is needed")
         if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
             raise ValueError(f"{name}: shape {tuple(t.shape)}, needed {shape}")
-        if not (t.is_contiguous() or (rows and (t.shape[0] == 0 or t[0].is_contiguous()))):
+        if not (t.is_contiguous() or (rows and _rows_fit(t))):
             raise ValueError(f"{name}: not contiguous")
-        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
-        return t
+        raise ValueError(f"{name}: on {t.device}, needed on CUDA device {'of the other tensors' if dev >= 0 else 'memory'}")
 
-    def _out(self, out):
-        p = self.problem
+    def _stream(self, dev, stream):
+        """The raw stream of a call whose tensors are on device `dev`, which must be the current one."""
+        if dev < 0 or dev != _current_device():
+            raise ValueError(f"the tensors are on {'the CPU' if dev < 0 else f'CUDA device {dev}'}, "
+                             "not on the current CUDA device")
+        return _raw_stream(dev) if stream is None else _stream(stream)
+
+    def _out(self, out, dev):
         if out is None:
-            return torch.empty((p.batch, p.num_q_heads, p.head_dim), dtype=torch.float32,
-                               device=torch.device("cuda", torch.cuda.current_device()))
-        return self._tensor("out", out, (torch.float32,), p.batch, p.num_q_heads, p.head_dim)
+            return torch.empty(self._q_shape, dtype=torch.float32, device=dev)
+        if not _fits(out, _F32, self._q_shape, dev):
+            self._refuse("out", out, _F32, self._q_shape, dev)
+        return out
 
     def split_workspace(self) -> torch.Tensor:
         """The workspace of window and kv4 calls (kept; calls that overlap need a Decoder each)."""
@@ -154,132 +189,184 @@ class Decoder:
             self._ws["split"] = torch.zeros(split_workspace_size(self.problem), dtype=torch.uint8, device=self.device)
         return self._ws["split"]
 
-    def _cache(self, name, t):
+    def _attend(self, kind, q, k, v, kv_indptr, pages, window, sinks, out, debug, stream):
+        dev = q.get_device()
+        if not _fits(q, self._dt, self._q_shape, dev):
+            self._refuse("q", q, self._dt, self._q_shape, dev)
+        if kind == "window":
+            for name, t in (("k", k), ("v", v)):
+                if not _fits(t, self._dt, self._kv_shape, dev):
+                    self._refuse(name, t, self._dt, self._kv_shape, dev)
+        elif not _fits(k, _U8, self._kv4_shape, dev):
+            self._refuse("kv4", k, _U8, self._kv4_shape, dev)
         p = self.problem
-        return self._tensor(name, t, self._dtypes(), p.total_tokens, p.num_kv_heads, p.head_dim)
-
-    def _kv4_cache(self, t):
-        p = self.problem
-        return self._tensor("kv4", t, (torch.uint8,), p.total_tokens, p.num_kv_heads, p.head_dim + p.head_dim // 8)
-
-    def _query(self, q):
-        p = self.problem
-        return self._tensor("q", q, self._dtypes(), p.batch, p.num_q_heads, p.head_dim)
-
-    def _indptr(self, t):
-        return self._tensor("kv_indptr", t, (torch.int64,), self.problem.batch + 1)
-
-    def _pages(self, page_table, kv_lens, page_size):
-        p = self.problem
-        self._tensor("page_table", page_table, (torch.int32,), p.batch, None)
-        self._tensor("kv_lens", kv_lens, (torch.int32,), p.batch)
-        if page_size < 1 or p.total_tokens % page_size:
-            raise ValueError(f"page_size {page_size} does not divide total_tokens {p.total_tokens}")
-        return make_pages(page_table, kv_lens, page_size, p.total_tokens // page_size)
+        indptr = pref = None
+        if pages is None:
+            if not _fits(kv_indptr, _I64, (p.batch + 1,), dev):
+                self._refuse("kv_indptr", kv_indptr, _I64, (p.batch + 1,), dev)
+            indptr = kv_indptr.data_ptr()
+        else:
+            table, lens, size = pages
+            if table.dim() != 2 or not _fits(table, _I32, (p.batch, table.shape[1]), dev):
+                self._refuse("page_table", table, _I32, (p.batch, None), dev)
+            if not _fits(lens, _I32, (p.batch,), dev):
+                self._refuse("kv_lens", lens, _I32, (p.batch,), dev)
+            if size < 1 or p.total_tokens % size:
+                raise ValueError(f"page_size {size} does not divide total_tokens {p.total_tokens}")
+            pref = ctypes.byref(Pages(table.data_ptr(), lens.data_ptr(), size, table.shape[1], p.total_tokens // size))
+        out = self._out(out, dev)
+        w = self._windows.get((window, sinks))
+        if w is None:
+            w = self._windows[(window, sinks)] = ctypes.byref(Window(window, sinks))
+        ws = self._ws.get("split")
+        if ws is None:
+            ws = self.split_workspace()
+        st = self._stream(dev, stream)
+        dbg = None if debug is None else ctypes.byref(debug)
+        L = lib()
+        if kind == "window":
+            _check("santa_decode_window", L.santa_decode_window(
+                self._pref, w, pref, q.data_ptr(), k.data_ptr(), v.data_ptr(), indptr, out.data_ptr(), ws.data_ptr(),
+                ws.numel(), dbg, st))
+        else:
+            _check("santa_decode_kv4", L.santa_decode_kv4(
+                self._pref, w, pref, q.data_ptr(), k.data_ptr(), indptr, out.data_ptr(), ws.data_ptr(), ws.numel(), dbg, st))
+        return out
 
     def window(self, q, k, v, kv_indptr, window, sinks=0, out=None, debug=None, stream=None) -> torch.Tensor:
         """Exact decode over the last `window` keys and the first `sinks` (santa_decode_window); window 0: all."""
-        out = self._out(out)
-        santa_decode_window(self.problem, Window(window, sinks), self._query(q), self._cache("k", k),
-                            self._cache("v", v), self._indptr(kv_indptr), out, self.split_workspace(), None, debug,
-                            stream)
-        return out
+        return self._attend("window", q, k, v, kv_indptr, None, window, sinks, out, debug, stream)
 
     def window_paged(self, q, k_pool, v_pool, page_table, kv_lens, page_size, window, sinks=0, out=None, debug=None,
                      stream=None) -> torch.Tensor:
         """The same on a paged cache; total_tokens must be the pools' rows, num_pages * page_size."""
-        out = self._out(out)
-        santa_decode_window(self.problem, Window(window, sinks), self._query(q), self._cache("k_pool", k_pool),
-                            self._cache("v_pool", v_pool), None, out, self.split_workspace(),
-                            self._pages(page_table, kv_lens, page_size), debug, stream)
-        return out
-
-    def kv4_cache(self) -> torch.Tensor:
-        """An empty 4-bit cache for the problem's total_tokens: [rows][Hkv][d + d / 8] bytes."""
-        p = self.problem
-        kv4_size(p)  # checks the problem
-        return torch.zeros((p.total_tokens, p.num_kv_heads, p.head_dim + p.head_dim // 8), dtype=torch.uint8,
-                           device=self.device)
-
-    def _slots(self, slot_map, n):
-        return None if slot_map is None else self._tensor("slot_map", slot_map, (torch.int64,), n)
-
-    def kv4_append(self, k, v, slot_map, kv4, debug=None, stream=None) -> torch.Tensor:
-        """Stores tokens k, v [tokens][Hkv][d] into rows slot_map of the 4-bit cache (santa_kv4_append)."""
-        p = self.problem
-        self._tensor("k", k, self._dtypes(), None, p.num_kv_heads, p.head_dim, rows=True)
-        self._tensor("v", v, self._dtypes(), k.shape[0], p.num_kv_heads, p.head_dim, rows=True)
-        santa_kv4_append(p, k, v, self._slots(slot_map, k.shape[0]), self._kv4_cache(kv4), debug, stream)
-        return kv4
-
-    def kv4_read(self, kv4, slot_map, k_out=None, v_out=None, debug=None, stream=None):
-        """Rows slot_map of the 4-bit cache as (k, v) [tokens][Hkv][d] (santa_kv4_read)."""
-        p, n = self.problem, slot_map.shape[0]
-        self._kv4_cache(kv4)
-        k_out, v_out = (torch.empty((n, p.num_kv_heads, p.head_dim), dtype=self._dtypes()[0], device=kv4.device)
-                        if t is None else self._tensor(name, t, self._dtypes(), n, p.num_kv_heads, p.head_dim)
-                        for name, t in (("k_out", k_out), ("v_out", v_out)))
-        santa_kv4_read(p, n, kv4, self._slots(slot_map, n), k_out, v_out, debug, stream)
-        return k_out, v_out
+        return self._attend("window", q, k_pool, v_pool, None, (page_table, kv_lens, page_size), window, sinks, out, debug,
+                            stream)
 
     def kv4(self, q, kv4, kv_indptr, window=0, sinks=0, out=None, debug=None, stream=None) -> torch.Tensor:
         """Exact decode over the 4-bit cache (santa_decode_kv4)."""
-        out = self._out(out)
-        santa_decode_kv4(self.problem, Window(window, sinks), self._query(q), self._kv4_cache(kv4),
-                         self._indptr(kv_indptr), out, self.split_workspace(), None, debug, stream)
-        return out
+        return self._attend("kv4", q, kv4, None, kv_indptr, None, window, sinks, out, debug, stream)
 
     def kv4_paged(self, q, kv4, page_table, kv_lens, page_size, window=0, sinks=0, out=None, debug=None,
                   stream=None) -> torch.Tensor:
         """The same on a paged 4-bit cache."""
-        out = self._out(out)
-        santa_decode_kv4(self.problem, Window(window, sinks), self._query(q), self._kv4_cache(kv4), None, out,
-                         self.split_workspace(), self._pages(page_table, kv_lens, page_size), debug, stream)
-        return out
+        return self._attend("kv4", q, kv4, None, None, (page_table, kv_lens, page_size), window, sinks, out, debug, stream)
+
+    def kv4_cache(self) -> torch.Tensor:
+        """An empty 4-bit cache for the problem's total_tokens: [rows][Hkv][d + d / 8] bytes."""
+        kv4_size(self.problem)  # checks the problem
+        return torch.zeros(self._kv4_shape, dtype=torch.uint8, device=self.device)
+
+    def _slots(self, slot_map, n, dev):
+        if slot_map is None:
+            return None
+        if not _fits(slot_map, _I64, (n,), dev):
+            self._refuse("slot_map", slot_map, _I64, (n,), dev)
+        return slot_map.data_ptr()
+
+    def _rows(self, name, t, n, heads, dev):
+        """(address, elements from token to token) of [tokens][heads][d], whose tokens may lie apart."""
+        shape = (n, heads, self.problem.head_dim)
+        if t.dtype not in self._dt or t.shape != shape or t.get_device() != dev or not _rows_fit(t):
+            self._refuse(name, t, self._dt, shape, dev, rows=True)
+        return t.data_ptr(), t.stride(0) if n > 1 else heads * shape[2]
+
+    def kv4_append(self, k, v, slot_map, kv4, debug=None, stream=None) -> torch.Tensor:
+        """Stores tokens k, v [tokens][Hkv][d] into rows slot_map of the 4-bit cache (santa_kv4_append)."""
+        h, n, dev = self.problem.num_kv_heads, k.shape[0], k.get_device()
+        kp, ks = self._rows("k", k, n, h, dev)
+        vp, vs = self._rows("v", v, n, h, dev)
+        slots = self._slots(slot_map, n, dev)
+        if not _fits(kv4, _U8, self._kv4_shape, dev):
+            self._refuse("kv4", kv4, _U8, self._kv4_shape, dev)
+        _check("santa_kv4_append", lib().santa_kv4_append(
+            self._pref, n, kp, ks, vp, vs, slots, kv4.data_ptr(),
+            None if debug is None else ctypes.byref(debug), self._stream(dev, stream)))
+        return kv4
+
+    def kv4_read(self, kv4, slot_map, k_out=None, v_out=None, debug=None, stream=None):
+        """Rows slot_map of the 4-bit cache as (k, v) [tokens][Hkv][d] (santa_kv4_read)."""
+        p, n, dev = self.problem, slot_map.shape[0], kv4.get_device()
+        shape = (n, p.num_kv_heads, p.head_dim)
+        if not _fits(kv4, _U8, self._kv4_shape, dev):
+            self._refuse("kv4", kv4, _U8, self._kv4_shape, dev)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16 if p.dtype == BF16 else torch.float32, device=dev)
+        elif not _fits(k_out, self._dt, shape, dev):
+            self._refuse("k_out", k_out, self._dt, shape, dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16 if p.dtype == BF16 else torch.float32, device=dev)
+        elif not _fits(v_out, self._dt, shape, dev):
+            self._refuse("v_out", v_out, self._dt, shape, dev)
+        _check("santa_kv4_read", lib().santa_kv4_read(
+            self._pref, n, kv4.data_ptr(), self._slots(slot_map, n, dev), k_out.data_ptr(), v_out.data_ptr(),
+            None if debug is None else ctypes.byref(debug), self._stream(dev, stream)))
+        return k_out, v_out
 
     def norm_rope(self, q, k, v, positions, slot_map, cos_sin, k_cache, v_cache, q_weight=None, k_weight=None,
                   eps=1e-6, interleaved=False, out=None, debug=None, stream=None):
         """Norms and rotation of the step's q [tokens][Hq][d] and k [tokens][Hkv][d]; k and v go to rows slot_map
         of the caches (santa_norm_rope).  cos_sin: rope_table.  Returns the rotated queries.  q, or k with
         k_cache, or v with v_cache may be None."""
-        p, dt = self.problem, self._dtypes()
-        n = next((t.shape[0] for t in (q, k, v) if t is not None), 0)
-        for name, t, heads in (("q", q, p.num_q_heads), ("k", k, p.num_kv_heads), ("v", v, p.num_kv_heads)):
-            if t is not None:
-                self._tensor(name, t, dt, n, heads, p.head_dim, rows=True)
-        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if t is not None:
-                self._tensor(name, t, dt, p.head_dim)
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if t is not None:
-                self._cache(name, t)
-        self._tensor("positions", positions, (torch.int32,), n)
-        self._tensor("cos_sin", cos_sin, (torch.float32,), None, None)
+        p, dev = self.problem, positions.get_device()
+        n, d = positions.shape[0], p.head_dim
+        if not _fits(positions, _I32, (n,), dev):
+            self._refuse("positions", positions, _I32, (None,), dev)
+        if cos_sin.dim() != 2 or not _fits(cos_sin, _F32, cos_sin.shape, dev):
+            self._refuse("cos_sin", cos_sin, _F32, (None, None), dev)
+        qp = kp = vp = op = kc = vc = qw = kw = None
+        qs = ks = vs = 0
         if q is not None:
+            qp, qs = self._rows("q", q, n, p.num_q_heads, dev)
+            shape = (n, p.num_q_heads, d)
             if out is None:
-                out = torch.empty((n, p.num_q_heads, p.head_dim), dtype=q.dtype, device=q.device)
-            self._tensor("out", out, dt, n, p.num_q_heads, p.head_dim)
-        r = Rope(None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-                 eps, cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
-        santa_norm_rope(p, r, q, k, v, positions, self._slots(slot_map, n), out if q is not None else None, k_cache,
-                        v_cache, debug, stream)
+                out = torch.empty(shape, dtype=q.dtype, device=dev)
+            elif not _fits(out, self._dt, shape, dev):
+                self._refuse("out", out, self._dt, shape, dev)
+            op = out.data_ptr()
+        if k is not None:
+            kp, ks = self._rows("k", k, n, p.num_kv_heads, dev)
+        if v is not None:
+            vp, vs = self._rows("v", v, n, p.num_kv_heads, dev)
+        if k_cache is not None:
+            if not _fits(k_cache, self._dt, self._kv_shape, dev):
+                self._refuse("k_cache", k_cache, self._dt, self._kv_shape, dev)
+            kc = k_cache.data_ptr()
+        if v_cache is not None:
+            if not _fits(v_cache, self._dt, self._kv_shape, dev):
+                self._refuse("v_cache", v_cache, self._dt, self._kv_shape, dev)
+            vc = v_cache.data_ptr()
+        if q_weight is not None:
+            if not _fits(q_weight, self._dt, (d,), dev):
+                self._refuse("q_weight", q_weight, self._dt, (d,), dev)
+            qw = q_weight.data_ptr()
+        if k_weight is not None:
+            if not _fits(k_weight, self._dt, (d,), dev):
+                self._refuse("k_weight", k_weight, self._dt, (d,), dev)
+            kw = k_weight.data_ptr()
+        r = Rope(qw, kw, eps, cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], bool(interleaved))
+        _check("santa_norm_rope", lib().santa_norm_rope(
+            self._pref, ctypes.byref(r), n, qp, qs, kp, ks, vp, vs, positions.data_ptr(), self._slots(slot_map, n, dev), op,
+            kc, vc, None if debug is None else ctypes.byref(debug), self._stream(dev, stream)))
         return out
 
     def page_plan(self, kv_lens, new_lens, page_table, free_pages, page_size, slot_map, positions, lens_out, counts,
                   debug=None, stream=None) -> None:
         """Pages, cache rows and positions for the step's new tokens (santa_page_plan); page_table is
         updated in place, slot_map, positions, lens_out and counts are written."""
-        p, i32 = self.problem, (torch.int32,)
-        self._tensor("kv_lens", kv_lens, i32, None)
-        n = kv_lens.shape[0]
-        self._tensor("new_lens", new_lens, i32, n)
-        self._tensor("page_table", page_table, i32, n, None)
-        self._tensor("free_pages", free_pages, i32, None)
-        self._tensor("slot_map", slot_map, (torch.int64,), None)
-        self._tensor("positions", positions, i32, slot_map.shape[0])
-        self._tensor("lens_out", lens_out, i32, n)
-        self._tensor("counts", counts, i32, 2)
-        if page_size < 1 or p.total_tokens % page_size:
-            raise ValueError(f"page_size {page_size} does not divide total_tokens {p.total_tokens}")
-        santa_page_plan(page_size, p.total_tokens // page_size, kv_lens, new_lens, page_table, free_pages, slot_map,
-                        positions, lens_out, counts, debug, stream)
+        rows, dev = self.problem.total_tokens, kv_lens.get_device()
+        n, tokens, free = kv_lens.numel(), slot_map.numel(), free_pages.numel()
+        if page_size < 1 or rows % page_size:
+            raise ValueError(f"page_size {page_size} does not divide total_tokens {rows}")
+        pages = page_table.shape[-1]
+        for name, t, dtypes, shape in (
+                ("kv_lens", kv_lens, _I32, (n,)), ("new_lens", new_lens, _I32, (n,)),
+                ("page_table", page_table, _I32, (n, pages)), ("free_pages", free_pages, _I32, (free,)),
+                ("slot_map", slot_map, _I64, (tokens,)), ("positions", positions, _I32, (tokens,)),
+                ("lens_out", lens_out, _I32, (n,)), ("counts", counts, _I32, (2,))):
+            if not _fits(t, dtypes, shape, dev):
+                self._refuse(name, t, dtypes, shape, dev)
+        _check("santa_page_plan", lib().santa_page_plan(
+            n, page_size, pages, rows // page_size, kv_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(),
+            free_pages.data_ptr(), free, slot_map.data_ptr(), positions.data_ptr(), tokens, lens_out.data_ptr(),
+            counts.data_ptr(), None if debug is None else ctypes.byref(debug), self._stream(dev, stream)))
