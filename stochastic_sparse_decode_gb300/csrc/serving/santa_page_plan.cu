@@ -7,7 +7,9 @@
 // Every CTA scans the sequences itself, kPlanThreads at a time (two block scans: the
 // token counts, which decide who fits, then the page counts of those that do), so no
 // CTA waits for another and one launch does it all; the CTAs then share the tile's new
-// pages and tokens, each found by a binary search in the tile's prefix sums.  A page
+// pages and tokens, found by binary searches in the tile's prefix sums: four consecutive
+// tokens per thread and search, written by 16-byte stores, with the page of a position by
+// multiplication (the divisor is the call's).  A page
 // that a token lies in is read from the free list itself when it is new, so the table
 // entries that another CTA writes are never read.
 #include "santa_serving.h"
@@ -56,6 +58,12 @@ __device__ __forceinline__ int upper(const long long *end, int n, long long x) {
             lo = mid + 1;
     }
     return lo;
+}
+
+// pos / page_size, by the magic number of the launch: floor(pos (2^s / d rounded up) / 2^s) with
+// s = 31 + ceil(log2 d) is the quotient for every 0 <= pos < 2^31.
+__device__ __forceinline__ int page_of(int pos, const PlanParams &p) {
+    return p.page_size == 1 ? pos : int(__umulhi(unsigned(pos), p.magic) >> p.shift);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p) {
@@ -107,24 +115,41 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
             const int k = int(i - (s > 0 ? s_page[s - 1] : 0));
             p.page_table[(size_t)(b0 + s) * p.max_pages + s_have[s] + k] = p.free_pages[page0 + i];
         }
-        for (long long i = me; i < tile_tok; i += all) {
-            if (tok0 + i >= p.max_tokens) break;
-            const int s = upper(s_tok, nb, i);
-            const long long first = s > 0 ? s_tok[s - 1] : 0;
-            long long slot = -1;
-            int pos = 0;
-            if (s_ok[s]) {
-                pos = s_len[s] + int(i - first);
-                const int pg = pos / p.page_size, fresh = pg - s_have[s];
-                const int id = fresh >= 0 ? p.free_pages[page0 + (s > 0 ? s_page[s - 1] : 0) + fresh]
+        // tokens tok0 .. tok0 + tile_tok - 1, by groups of four that start at a multiple of four
+        const long long row_end = min(tok0 + tile_tok, (long long)p.max_tokens);
+        for (long long i0 = (tok0 & ~3LL) + 4 * me; i0 < row_end; i0 += 4 * all) {
+            long long slot[4];
+            int pos[4];
+            int s = upper(s_tok, nb, i0 > tok0 ? i0 - tok0 : 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                slot[j] = -1;
+                pos[j] = 0;
+                const long long i = i0 + j - tok0;
+                if (i0 + j >= row_end || i < 0) continue;
+                while (s_tok[s] <= i) ++s;  // ends: i < tile_tok
+                if (!s_ok[s]) continue;
+                pos[j] = s_len[s] + int(i - (s > 0 ? s_tok[s - 1] : 0));
+                const int pg = page_of(pos[j], p), fresh = pg - s_have[s];
+                const int id = fresh >= 0 ? __ldg(p.free_pages + page0 + (s > 0 ? s_page[s - 1] : 0) + fresh)
                                           : p.page_table[(size_t)(b0 + s) * p.max_pages + pg];
                 if (id >= 0 && id < p.num_pages)
-                    slot = (long long)id * p.page_size + pos % p.page_size;
+                    slot[j] = (long long)id * p.page_size + pos[j] - pg * p.page_size;
                 else
                     plan_flag(p, SANTA_ERR_INDPTR);
             }
-            p.slot_map[tok0 + i] = slot;
-            p.positions[tok0 + i] = pos;
+            if (i0 >= tok0 && i0 + 4 <= row_end) {
+                reinterpret_cast<longlong2 *>(p.slot_map + i0)[0] = make_longlong2(slot[0], slot[1]);
+                reinterpret_cast<longlong2 *>(p.slot_map + i0)[1] = make_longlong2(slot[2], slot[3]);
+                *reinterpret_cast<int4 *>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (i0 + j >= tok0 && i0 + j < row_end) {
+                        p.slot_map[i0 + j] = slot[j];
+                        p.positions[i0 + j] = pos[j];
+                    }
+            }
         }
         tok0 += tile_tok;
         page0 += tile_page;
@@ -142,7 +167,14 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
 
 }  // namespace
 
-cudaError_t launch_page_plan(const PlanParams &p, cudaStream_t stream) {
+cudaError_t launch_page_plan(const PlanParams &plan, cudaStream_t stream) {
+    PlanParams p = plan;
+    int log = 0;
+    while ((1LL << log) < p.page_size) ++log;
+    if (log > 0) {  // 2^(31 + log) / d < 2^32
+        p.magic = unsigned(((1ULL << (31 + log)) + p.page_size - 1) / p.page_size);
+        p.shift = log - 1;
+    }
     const int work = p.max_tokens > p.batch ? p.max_tokens : p.batch;
     int ctas = (work + kPlanThreads * 4 - 1) / (kPlanThreads * 4);
     ctas = ctas < 1 ? 1 : ctas > kPlanCtas ? kPlanCtas : ctas;

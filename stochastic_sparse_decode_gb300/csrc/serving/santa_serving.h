@@ -16,6 +16,7 @@ struct PlanParams {
     long long *slot_map;
     int *positions, *lens_out, *counts;
     unsigned int *err;
+    unsigned magic, shift;  // division by page_size (set by the launcher)
 };
 cudaError_t launch_page_plan(const PlanParams &p, cudaStream_t stream);
 
