@@ -499,9 +499,8 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                                     mma_f16(acc, a & kLo, a & kHi, c & kLo, c & kHi, b[2 * ks], b[2 * ks + 1]);
                             }
                         float(&o)[4] = O[4 * i + 2 * half + s];
-                        const float2 lo = __ffma2_rn(make_float2(o[0], o[1]), sco, make_float2(acc[0], acc[1]));
-                        const float2 hi = __ffma2_rn(make_float2(o[2], o[3]), sco, make_float2(acc[2], acc[3]));
-                        o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[j] = fmaf(o[j], j & 1 ? sco.y : sco.x, acc[j]);
                     }
                 }
             if (!kTma && more) load_v(next, next_seen);

@@ -28,7 +28,7 @@ namespace santa {
 namespace {
 
 constexpr int kStoreThreads = 256;
-constexpr int kMany = 4;
+constexpr int kMany = 2;
 constexpr float kHalfMax = 65504.f;
 
 // The rows of a token are K of its KV heads, then V.  A lane row (D / 8 lanes) takes row

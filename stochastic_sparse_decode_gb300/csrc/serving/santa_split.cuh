@@ -109,6 +109,7 @@ struct Walk {
     int n, run;   // block of the head; where its run of consecutive keys ends
     int key0;     // the block's first key
     int in_page;  // paged: where in its page the block begins
+    int ahead;    // paged: the page table's next entry (loaded a page ahead of its use)
     int row;      // its first cache row; -1: a bad page id (flagged), its keys are dropped
     int sel;      // the head: heads[sel]
     Head *heads;  // [2], the warp's own
@@ -120,13 +121,32 @@ __device__ __forceinline__ void put_head(Walk &w, int slot, const Head &h) {
     if ((threadIdx.x & 31) == 0) w.heads[slot] = h;
     __syncwarp();
 }
+// The first cache row of a page, -1 (flagged) for a bad id.
+__device__ __forceinline__ int page_row(const Params &p, int id) {
+    if (id >= 0 && id < p.num_pages) return id * p.page_size;
+    raise_flag(p, SANTA_ERR_INDPTR);
+    return -1;
+}
+// Loads the table's entry behind the page of w.key0, if the row has one.
+__device__ __forceinline__ void look_ahead(const Params &p, Walk &w, int b) {
+    const int i = (w.key0 - w.in_page) / p.page_size + 1;
+    w.ahead = i < p.max_pages ? __ldg(p.page_table + (size_t)b * p.max_pages + i) : -1;
+}
 // The run and the row of block w.n of h, by the page table.
 template <bool kPaged>
 __device__ __forceinline__ void place(const SplitParams &sp, Walk &w, const Head &h) {
+    const Params &p = sp.p;
     w.run = w.n < h.nsb ? h.nsb : h.nb;
     w.key0 = h.first_key(w.n);
-    w.row = int(key_row<kPaged>(sp.p, h.b, h.start, w.key0));
-    if constexpr (kPaged) w.in_page = w.key0 % sp.p.page_size;
+    if constexpr (kPaged) {
+        const int page = w.key0 / p.page_size;
+        w.in_page = w.key0 - page * p.page_size;
+        w.row = page_row(p, __ldg(p.page_table + (size_t)h.b * p.max_pages + page));
+        if (w.row >= 0) w.row += w.in_page;
+        look_ahead(p, w, h.b);
+    } else {
+        w.row = h.start + w.key0;
+    }
 }
 // Which of the 32 keys of the walk's block the query sees, a bit each.
 __device__ __forceinline__ unsigned seen_bits(const Walk &w) {
@@ -170,17 +190,19 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         return ctas;
     };
     int ctas;
+    Head h;
     if (p.B <= 128) {  // every warp scans for itself: no barrier
-        int nb[4];
+        int nb[4], len[4], from[4];
         long long end[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            nb[k] = 0;
+            nb[k] = len[k] = from[k] = 0;
             if (32 * k < p.B) {
-                Head h;
                 if (32 * k + lane < p.B) {
                     load_head<kPaged>(h, sp, 32 * k + lane);
                     nb[k] = h.nb;
+                    len[k] = h.vis.L;
+                    from[k] = h.start;
                 }
                 unsigned empty = __ballot_sync(kFull, 32 * k + lane < p.B && nb[k] == 0);
                 while (empty) {
@@ -208,8 +230,12 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                         const int l = __ffs(past) - 1;
                         b = 32 * k + l;
                         prefix = __shfl_sync(kFull, end[k] - nb[k], l);
+                        h.start = __shfl_sync(kFull, from[k], l);
+                        h.vis.L = __shfl_sync(kFull, len[k], l);
                     }
                 }
+            h.b = b;
+            set_blocks(h, h.vis.L, sp);
         }
     } else {
         constexpr int NT = NW * 32;
@@ -232,7 +258,6 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
             return v + before;
         };
         for (int b0 = 0; b0 < p.B; b0 += NT) {
-            Head h;
             h.nb = 0;
             if (b0 + (int)threadIdx.x < p.B) load_head<kPaged>(h, sp, b0 + threadIdx.x);
             long long all;
@@ -246,7 +271,6 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         }
         long long carry = 0;
         for (int b0 = 0; b0 < p.B; b0 += NT) {
-            Head h;
             h.nb = 0;
             const int mine = b0 + threadIdx.x;
             if (mine < p.B) load_head<kPaged>(h, sp, mine);
@@ -276,8 +300,7 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         w.left = 0;
         return 0;
     }
-    Head h;
-    load_head<kPaged>(h, sp, b);
+    if (p.B > 128) load_head<kPaged>(h, sp, b);
     const long long rem = x - prefix * p.Hkv;
     h.kvh = int(divide(rem, h.nb));
     w.n = int(rem - (long long)h.kvh * h.nb);
@@ -304,12 +327,16 @@ __device__ __forceinline__ int next_unit(const SplitParams &sp, Walk &w) {
             w.in_page += kBlock;
             if (w.in_page < sp.p.page_size) {
                 if (w.row >= 0) w.row += kBlock;
-                return 1;
+            } else {
+                w.in_page = 0;
+                w.row = page_row(sp.p, w.ahead);
+                look_ahead(sp.p, w, w.heads[w.sel].b);
             }
+            return 1;
         }
     }
     Head h = w.heads[w.sel];
-    if (w.n < h.nb) {  // another page, or from the sinks to the window
+    if (w.n < h.nb) {  // from the sinks to the window
         place<kPaged>(sp, w, h);
         return 1;
     }
