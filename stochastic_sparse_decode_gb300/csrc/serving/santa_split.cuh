@@ -7,7 +7,8 @@
 // batch in the order (sequence, KV head, block) are cut into equal contiguous stretches,
 // one per warp of the grid, so that every warp has the same number of units, to one,
 // whatever the lengths are; lengths are read on the device, and each warp works out its
-// own stretch.  A warp keeps an online softmax (M, Z, O) per query head and closes it
+// own stretch.  (When the heads are no more than the CTAs and none is longer than a CTA reads
+// in two rounds, each CTA takes one head instead, and nothing is joined across CTAs.)  A warp keeps an online softmax (M, Z, O) per query head and closes it
 // when its stretch leaves a head:
 //   - a head that lies within the stretch is finished by the warp itself;
 //   - a head shared by warps of one CTA only is joined through shared memory;
@@ -26,6 +27,7 @@ namespace santa {
 
 constexpr int kBlock = 32;         // keys per unit
 constexpr int kMinUnitsPerCta = 4; // fewer CTAs than the grid has while a CTA would get less
+constexpr int kWholeUnits = 2;     // a head of at most so many units per warp stays in one CTA if all do
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -92,7 +94,7 @@ struct SplitShared {
     int list[2 * NW + 1];                              // the pieces there are, in order
     int begin[2 * NW + 1];                             // where in `list` each head's pieces begin
     long long inc_u0[2];                               // the CTA's heads that others share: first, last
-    int inc_b[2], inc_kvh[2], inc_nb[2], inc_first[2], inc_parts[2], last[2];
+    int inc_b[2], inc_kvh[2], inc_first[2], inc_parts[2], last[2];
     long long X, cta0, cta1;                           // units of the batch; the CTA's stretch
     int ctas;                                          // CTAs that have a stretch
     long long x0[NW];                                  // plan of a large batch: where the warps start
@@ -170,29 +172,27 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
     long long total = 0, prefix = 0, x = 0;
     int b = -1;
     w.left = 0;
-    auto ranges = [&]() {
-        const long long X = total * p.Hkv, most = (X + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
-        const int ctas = most < (long long)gridDim.x ? int(most) : int(gridDim.x);
-        long long cta0 = X, cta1 = X;
-        if ((int)blockIdx.x < ctas) {
-            cta0 = stretch_start(X, ctas, blockIdx.x);
-            cta1 = stretch_start(X, ctas, blockIdx.x + 1);
-            const long long from = stretch_start(cta1 - cta0, NW, warp);
-            x = cta0 + from;
-            w.left = int(stretch_start(cta1 - cta0, NW, warp + 1) - from);
-        }
+    int ctas;  // that have a stretch
+    // The CTA's stretch is cta0 .. cta1 - 1; the warp's, an equal part of it.
+    auto take = [&](long long X, long long cta0, long long cta1) {
+        const long long from = stretch_start(cta1 - cta0, NW, warp);
+        x = cta0 + from;
+        w.left = int(stretch_start(cta1 - cta0, NW, warp + 1) - from);
         if (threadIdx.x == 0) {
             sh.X = X;
             sh.cta0 = cta0;
             sh.cta1 = cta1;
             sh.ctas = ctas;
         }
-        return ctas;
     };
-    int ctas;
+    auto equal_stretches = [&]() {
+        const long long X = total * p.Hkv, most = (X + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
+        ctas = most < (long long)gridDim.x ? int(most) : int(gridDim.x);
+        if ((int)blockIdx.x < ctas) take(X, stretch_start(X, ctas, blockIdx.x), stretch_start(X, ctas, blockIdx.x + 1));
+    };
     Head h;
     if (p.B <= 128) {  // every warp scans for itself: no barrier
-        int nb[4], len[4], from[4];
+        int nb[4], len[4], from[4], most = 0;
         long long end[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -204,6 +204,7 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                     len[k] = h.vis.L;
                     from[k] = h.start;
                 }
+                most = max(most, nb[k]);
                 unsigned empty = __ballot_sync(kFull, 32 * k + lane < p.B && nb[k] == 0);
                 while (empty) {
                     const int e = 32 * k + __ffs(empty) - 1;
@@ -213,14 +214,36 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                 long long v = nb[k];
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
+                    if (o >= p.B) break;
                     const long long u = __shfl_up_sync(kFull, v, o);
                     if (lane >= o) v += u;
                 }
                 end[k] = total + v;
-                total = __shfl_sync(kFull, end[k], 31);
+                total = __shfl_sync(kFull, end[k], min(31, p.B - 32 * k - 1));
             }
         }
-        ctas = ranges();
+        if (p.B * p.Hkv <= (int)gridDim.x && warp_max_int(most) <= kWholeUnits * NW) {
+            // few short heads: a CTA each
+            ctas = p.B * p.Hkv;
+            if ((int)blockIdx.x < ctas) {
+                b = blockIdx.x / p.Hkv;
+                const int kvh = blockIdx.x - b * p.Hkv;
+                int n = 0;
+                long long e = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (b / 32 == k) {
+                        n = __shfl_sync(kFull, nb[k], b % 32);
+                        e = __shfl_sync(kFull, end[k], b % 32);
+                    }
+                if (n == 0) return -1;
+                const long long cta0 = (e - n) * p.Hkv + (long long)kvh * n;
+                take(total * p.Hkv, cta0, cta0 + n);
+            }
+        } else {
+            equal_stretches();
+        }
+        if ((int)blockIdx.x >= ctas) return -1;
         if (w.left > 0) {
 #pragma unroll
             for (int k = 3; k >= 0; --k)
@@ -264,7 +287,7 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
             block_scan(h.nb, &all);
             total += all;
         }
-        ctas = ranges();
+        equal_stretches();
         if (lane == 0) {
             sh.x0[warp] = w.left > 0 ? x : -1;
             sh.start_b[warp] = -1;
@@ -382,11 +405,13 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
     // the pieces there are, and where each head's begin (every warp finds the same)
     const long long my_u0 = lane < 2 * NW ? sh.u0[lane] : -1;
     const unsigned valid = __ballot_sync(kFull, my_u0 >= 0);
-    const unsigned mates = __match_any_sync(kFull, my_u0) & valid;
-    const unsigned heads = __ballot_sync(kFull, my_u0 >= 0 && __ffs(mates) - 1 == lane);
+    // pieces come in the order of the units, so a head's are neighbours among those there are
+    const unsigned below = valid & ((1u << lane) - 1);
+    const long long before = __shfl_sync(kFull, my_u0, below ? 31 - __clz(below) : lane);
+    const unsigned heads = __ballot_sync(kFull, my_u0 >= 0 && (!below || before != my_u0));
     const int n_heads = __popc(heads);
     if (warp == 0) {
-        const int at = __popc(valid & ((1u << lane) - 1));
+        const int at = __popc(below);
         if (my_u0 >= 0) sh.list[at] = lane;
         if (heads >> lane & 1) sh.begin[__popc(heads & ((1u << lane) - 1))] = at;
         if (lane == 0) sh.begin[n_heads] = __popc(valid);
@@ -396,8 +421,8 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
         unsigned rest = heads;
         for (int q = 0; q < k; ++q) rest &= rest - 1;
         const int i = __ffs(rest) - 1;  // the head's first piece
-        const bool in = __shfl_sync(kFull, mates, i) >> lane & 1;
         const long long u0 = __shfl_sync(kFull, my_u0, i);
+        const bool in = my_u0 == u0;
         const float m = in ? sh.M[lane][h] : -INFINITY;
         const float M = warp_max(m), Mref = M == -INFINITY ? 0.f : M;
         float c = in ? ex2(m - Mref) : 0.f;
@@ -411,7 +436,9 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
                 sh.inc_u0[part] = u0;
                 sh.inc_b[part] = sh.b[i];
                 sh.inc_kvh[part] = sh.kvh[i];
-                sh.inc_nb[part] = sh.nb[i];
+                const int first = stretch_of(sh.X, sh.ctas, u0);
+                sh.inc_first[part] = first;
+                sh.inc_parts[part] = stretch_of(sh.X, sh.ctas, u0 + sh.nb[i] - 1) - first + 1;
             }
         }
         if (in) sh.coef[lane][h] = c;
@@ -445,14 +472,10 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
         const int k = threadIdx.x;
         sh.last[k] = 0;
         if (sh.inc_u0[k] >= 0) {
-            const int first = stretch_of(sh.X, sh.ctas, sh.inc_u0[k]);
-            const int parts = stretch_of(sh.X, sh.ctas, sh.inc_u0[k] + sh.inc_nb[k] - 1) - first + 1;
-            sh.inc_first[k] = first;
-            sh.inc_parts[k] = parts;
             // the CTA's part is visible (the barrier above, this fence) before it is counted
             __threadfence();
             unsigned *cnt = sp.cnt + size_t(sh.inc_b[k]) * p.Hkv + sh.inc_kvh[k];
-            if (atomicAdd(cnt, 1u) == unsigned(parts - 1)) {
+            if (atomicAdd(cnt, 1u) == unsigned(sh.inc_parts[k] - 1)) {
                 sh.last[k] = 1;
                 *cnt = 0u;
                 __threadfence();  // the others' parts are read after their counts
