@@ -1,17 +1,22 @@
 // santa_kv4_attn.cu -- exact decode attention over a K/V cache held in 4 bits.
 //
 // A key row stands for k_i = m_g + s_g n_i (codes n_i in 0 .. 15; scale s_g and minimum m_g
-// of element i's group g), a value row likewise, so
-//   q . k_j       = sum_g s_jg (q_g . n_jg) + m_jg sum(q_g)
-//   sum_j e_j v_j = sum_j (e_j s_jg) n_j    + sum_j e_j m_jg          (group by group),
-// and both large products run on the tensor cores (fp16 mma m16n8k16) on the codes as
-// they lie in memory.  A code needs no conversion: masked out of its word it is, as an fp16
-// bit pattern, the subnormal n 2^-24 (low nibble of a byte) or n 2^-20 (high nibble), which
-// the tensor cores multiply exactly; the powers of two go into q and the final factor.
+// of element i's group g), a value row likewise.  With the codes centred, c = n - 8, and
+// m' = m + 8 s,
+//   q . k_j       = sum_g s_jg (q_g . c_jg) + m'_jg sum(q_g)
+//   sum_j e_j v_j = sum_j (e_j s_jg) c_j    + sum_j e_j m'_jg         (group by group),
+// and both large products run on the tensor cores (fp16 mma m16n8k16).  Two codes become an
+// fp16 pair by two instructions: masked out of the word into the low bits of 1024 (one LOP3),
+// then 1024 + n - 1032, or (1024 + 16 n) / 16 - 72 for the high nibble of a byte (one HFMA2),
+// both exact.  The centring is not for looks: with n itself the two terms of the second line
+// are each about 2.6 standard deviations of the values and cancel to the mean of thousands
+// of them, so that the last bits of the tensor cores' truncating sums showed as 3e-4 of the
+// output at 32768 keys; and codes used as they lie in memory, as fp16 subnormals n 2^-24 (no
+// second instruction), lose up to ten bits when products are aligned by their operands'
+// exponents.
 // Codes are the A operand of both (rows: keys, then elements), queries and weights the B
 // operand (columns: heads).  A word of K's codes gives a lane the A fragments of two products
-// (4 ands, 1 shift); two keys' words of V, paired by byte permutes, those of eight (2
-// permutes, 8 ands, 2 shifts).  The weights turn from the layout in which the logits come out
+// (1 shift besides); two keys' words of V, paired by byte permutes, those of eight.  The weights turn from the layout in which the logits come out
 // into the one in which they go in by movmatrix.
 //
 // Precision: q is scaled by a power of two per head to fit fp16 (a bf16 q is exact so; an
@@ -76,7 +81,18 @@ __device__ __forceinline__ int exponent(float x) {
     return e < -100 ? -100 : e > 100 ? 100 : e;
 }
 
-constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+// The low (or high) nibbles of bytes 0 and 2 of w, less 8, as an fp16 pair.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+    const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + n: the last bit of 1024 in fp16 is 1
+    const __half2 c = __hadd2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0xe408)));  // -1032
+    return *reinterpret_cast<const uint32_t *>(&c);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+    const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
+    const __half2 c = __hfma2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x2c00)),
+                              __half2half2(__ushort_as_half(0xd480)));  // / 16 - 72
+    return *reinterpret_cast<const uint32_t *>(&c);
+}
 
 template <int D, typename Q, int GT>
 struct Kv4Geom {
@@ -199,8 +215,8 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
     };
 
     // State of the heads of columns 2t, 2t + 1: M, the shares of the lane's own keys of Z and of
-    // the sums of e_j m_jg, and O^T: tile (word i of the lane's V words, q) holds elements 2q
-    // (O[..][0 .. 1]) and 2q + 1 (O[..][2 .. 3]) of word (kW / 2) g + i, times fscale 2^-24 and 2^-20.
+    // the sums of e_j m'_jg, and O^T: tile (word i of the lane's V words, q) holds elements 2q
+    // (O[..][0 .. 1]) and 2q + 1 (O[..][2 .. 3]) of word (kW / 2) g + i, times fscale.
     const int h0 = kTwice ? 2 * (t & 1) : 2 * t;  // head of column 2t
     float M[2], Z[2], base[kG][2], O[kTiles][4], fscale;
     auto reset = [&]() {
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) O[n][j] += __shfl_xor_sync(kFull, O[n][j], 2);
         }
-        const float f0 = 16777216.f / fscale, f1 = 1048576.f / fscale;  // powers of two
+        const float f = 1.f / fscale;  // a power of two
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int h = h0 + j;
@@ -238,8 +254,8 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) {
                     const int i = n / 4, at = 8 * (kW / 2 * g + i) + 2 * (n % 4);
-                    *reinterpret_cast<float2 *>(dst + at) = make_float2(fmaf(O[n][j], f0, base[i % kG][j]) * inv,
-                                                                        fmaf(O[n][2 + j], f1, base[i % kG][j]) * inv);
+                    *reinterpret_cast<float2 *>(dst + at) = make_float2(fmaf(O[n][j], f, base[i % kG][j]) * inv,
+                                                                        fmaf(O[n][2 + j], f, base[i % kG][j]) * inv);
                 }
                 if (!final && g == 0) {
                     sh.M[slot][h] = M[j];
@@ -283,7 +299,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             if (fresh) {
                 fresh = false;
                 // q as the B operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
-                // words kW t + u of the head of column g, the latter / 16 because their codes are high nibbles
+                // words kW t + u of the head of column g
                 const int hg = kTwice ? g & 3 : g;
                 const Q *qh = static_cast<const Q *>(p.q) +
                               (size_t(w.heads[sel].b) * p.Hq + w.heads[sel].kvh * G + min(hg, G - 1)) * D + t * kW * 8;
@@ -317,25 +333,25 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     for (int i = 0; i < kG; ++i) sum[i] += __shfl_xor_sync(kFull, sum[i], s);
                 }
                 const int e = exponent(mx);
-                const float f = pow2(14 - e), fh = f * 0.0625f;
+                const float f = pow2(14 - e);
 #pragma unroll
                 for (int u = 0; u < kW; ++u) {
                     float a[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * (i & 1 ? fh : f);
+                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * f;
 #pragma unroll
                     for (int part = 0; part < kQ; ++part)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) qf[part][u][i] = half_pair(a[i], a[i + 4]);
                 }
-                // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)), in the products' units
+                // y = sum_g s_g c_g + m'_g sum(q_g) / 2^(e - 14), in the products' units
                 const int e0 = __shfl_sync(kFull, e, 4 * h0), e1 = __shfl_sync(kFull, e, 4 * (h0 + 1));
                 const float scale2 = p.scale * 1.4426950408889634f;
-                kq = make_float2(pow2(e0 + 10) * scale2, pow2(e1 + 10) * scale2);
+                kq = make_float2(pow2(e0 - 14) * scale2, pow2(e1 - 14) * scale2);
 #pragma unroll
                 for (int i = 0; i < kG; ++i)
-                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(-10 - e0),
-                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(-10 - e1));
+                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(14 - e0),
+                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(14 - e1));
             }
             if constexpr (kTma) {
                 if (!mbar_wait(&bars[cur], phase >> cur & 1)) {
@@ -363,12 +379,13 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     fscale = f;
                 }
                 if (!kTma && more) load_par(next, next_seen);
-                // per key and group (s, s, m, m) of K, then of V; the slots of a key turn with the key
+                // per key and group (s, s, m', m') of K, then of V; the slots of a key turn with the key
                 // against bank conflicts
 #pragma unroll
                 for (int i = 0; i < 2 * kG; ++i) {
                     const float sc = i < kG ? sm[i].x : sm[i].x * fscale;
-                    par[lane * 2 * kG + ((i + lane) & (2 * kG - 1))] = make_float4(sc, sc, sm[i].y, sm[i].y);
+                    const float mid = fmaf(8.f, sm[i].x, sm[i].y);
+                    par[lane * 2 * kG + ((i + lane) & (2 * kG - 1))] = make_float4(sc, sc, mid, mid);
                 }
                 __syncwarp();
             }
@@ -391,10 +408,10 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                         for (int part = kQ - 1; part >= 0; --part) {
                             if (u < kG && s == 0 && part == kQ - 1)
-                                mma_f16_zero(c[u % kG], a & kLo, b & kLo, a & kHi, b & kHi, qf[part][u][2 * s],
+                                mma_f16_zero(c[u % kG], low_codes(a), low_codes(b), high_codes(a), high_codes(b), qf[part][u][2 * s],
                                              qf[part][u][2 * s + 1]);
                             else
-                                mma_f16(c[u % kG], a & kLo, b & kLo, a & kHi, b & kHi, qf[part][u][2 * s],
+                                mma_f16(c[u % kG], low_codes(a), low_codes(b), high_codes(a), high_codes(b), qf[part][u][2 * s],
                                         qf[part][u][2 * s + 1]);
                         }
                     }
@@ -494,9 +511,9 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                                 const uint32_t(&b)[4] = pf[i % kG][part];
                                 const uint32_t a = pr[2 * ks], c = pr[2 * ks + 1];
                                 if (ks == 0 && part == kParts - 1)
-                                    mma_f16_zero(acc, a & kLo, a & kHi, c & kLo, c & kHi, b[2 * ks], b[2 * ks + 1]);
+                                    mma_f16_zero(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks], b[2 * ks + 1]);
                                 else
-                                    mma_f16(acc, a & kLo, a & kHi, c & kLo, c & kHi, b[2 * ks], b[2 * ks + 1]);
+                                    mma_f16(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks], b[2 * ks + 1]);
                             }
                         float(&o)[4] = O[4 * i + 2 * half + s];
 #pragma unroll

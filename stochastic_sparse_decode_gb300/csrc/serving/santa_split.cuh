@@ -7,8 +7,8 @@
 // batch in the order (sequence, KV head, block) are cut into equal contiguous stretches,
 // one per warp of the grid, so that every warp has the same number of units, to one,
 // whatever the lengths are; lengths are read on the device, and each warp works out its
-// own stretch.  (When the heads are no more than the CTAs and none is longer than a CTA reads
-// in two rounds, each CTA takes one head instead, and nothing is joined across CTAs.)  A warp keeps an online softmax (M, Z, O) per query head and closes it
+// own stretch.  (Where that costs more than it gives, kJoinUnits, each CTA takes one head
+// instead, and nothing is joined across CTAs.)  A warp keeps an online softmax (M, Z, O) per query head and closes it
 // when its stretch leaves a head:
 //   - a head that lies within the stretch is finished by the warp itself;
 //   - a head shared by warps of one CTA only is joined through shared memory;
@@ -27,7 +27,13 @@ namespace santa {
 
 constexpr int kBlock = 32;         // keys per unit
 constexpr int kMinUnitsPerCta = 4; // fewer CTAs than the grid has while a CTA would get less
-constexpr int kWholeUnits = 2;     // a head of at most so many units per warp stays in one CTA if all do
+// Joining a head's parts across CTAs costs about as much as a CTA's reading of this many
+// units (4 us; a unit adds 0.14 to 0.16 us to a CTA's time, bf16 or 4-bit, d = 128).  So when
+// the heads are no more than the CTAs, each takes one head whole unless the longest head is
+// longer than this and an equal share of all units together.  Batch 1, 8 KV heads, bf16, whole
+// against split: 256 keys 6.2 / 8.9 us, 768 8.9 / 9.4, 1024 10.2 / 9.6, 2048 15.0 / 9.9; batch
+// 16: 1024 keys 12.0 / 16.5, 2048 26.2 / 30.6.
+constexpr int kJoinUnits = 28;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -222,8 +228,8 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                 total = __shfl_sync(kFull, end[k], min(31, p.B - 32 * k - 1));
             }
         }
-        if (p.B * p.Hkv <= (int)gridDim.x && warp_max_int(most) <= kWholeUnits * NW) {
-            // few short heads: a CTA each
+        if (p.B * p.Hkv <= (int)gridDim.x &&
+            warp_max_int(most) <= kJoinUnits + divide(total * p.Hkv, int(gridDim.x))) {  // a CTA per head
             ctas = p.B * p.Hkv;
             if ((int)blockIdx.x < ctas) {
                 b = blockIdx.x / p.Hkv;

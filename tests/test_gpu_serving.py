@@ -442,6 +442,25 @@ def test_long_and_many(kind):
 
 
 @pytest.mark.parametrize("kind", ["window", "kv4"])
+@pytest.mark.parametrize("dtype,d,g", [("bf16", 128, 4), ("bf16", 128, 8), ("bf16", 64, 2), ("f32", 64, 4), ("f32", 128, 1)])
+def test_precision_of_means_over_many_keys(kind, dtype, d, g):
+    """The mean of many values is small against each of them, and errors that do not average out show.  Logits
+    here are below 8, formed to 8 2^-24 times a few roundings of each product's sum (about 1e-6), exponentials
+    to 2^-22, weights in parts of 22 bits or more: relative to the output, whose terms average like the errors,
+    2e-6 in all; twice that is allowed."""
+    for n in (100, 3000, 30000):
+        c = _attention_case(kind, dtype, d, 2, g, [n], 0, 0, 0, seed=n)
+        for h in range(2):
+            if kind == "kv4":
+                k, v = _values64(c["pools"][0][c["where"][0], h], d)
+            else:
+                k, v = (c["kv"][i][0][:, h].double() for i in range(2))
+            want = torch.softmax(c["q"][0, h * g:(h + 1) * g].double() @ k.T / math.sqrt(d), -1) @ v
+            err = float((c["out"][0, h * g:(h + 1) * g].double() - want).norm() / want.norm())
+            assert err <= 4e-6, (n, h, err)
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
 def test_large_logits_and_offsets(kind):
     """Logits of hundreds (weights that underflow) and keys with a common offset."""
     _check_attention(_attention_case(kind, "bf16", 128, 2, 4, [3000, 50], 0, 0, 0, seed=6, q_scale=20.0))
