@@ -19,7 +19,7 @@ namespace santa {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kPlanCtas = 304;  // two per SM
+constexpr int kPlanCtas = 304;  // two per SM (820k tokens: 152 13.0 us, 304 8.3, 608 10.6, 912 8.4)
 
 __device__ __forceinline__ void plan_flag(const PlanParams &p, unsigned bit) {
     if (p.err) atomicOr(p.err, bit);
@@ -71,12 +71,13 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     __shared__ long long s_tok[kPlanThreads], s_page[kPlanThreads];  // inclusive prefix sums of the tile
     __shared__ int s_len[kPlanThreads], s_have[kPlanThreads];
     __shared__ int s_ok[kPlanThreads];
+    __shared__ unsigned s_sum[2];  // pages taken, tokens placed (first CTA); both below 2^31
     const int tid = threadIdx.x;
     const long long me = (long long)blockIdx.x * kPlanThreads + tid, all = (long long)gridDim.x * kPlanThreads;
     pdl_wait();
     pdl_launch_dependents();
     long long tok0 = 0, page0 = 0;  // of the tiles before
-    long long taken = 0, placed = 0;
+    if (tid < 2) s_sum[tid] = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int len = 0, nw = 0;
@@ -103,11 +104,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
             p.lens_out[b] = ok ? len + nw : len > 0 ? len : 0;
             if (!ok) plan_flag(p, SANTA_ERR_PAGES);
         }
-        long long x;
-        block_scan(ok ? need : 0, scr, &x);  // its barriers also publish the arrays above
-        taken += x;
-        block_scan(ok ? n_tok : 0, scr, &x);
-        placed += x;
+        if (blockIdx.x == 0) {
+            const unsigned a = __reduce_add_sync(kFull, ok ? unsigned(need) : 0u);
+            const unsigned c = __reduce_add_sync(kFull, ok ? unsigned(n_tok) : 0u);
+            if ((tid & 31) == 0) {
+                atomicAdd(&s_sum[0], a);
+                atomicAdd(&s_sum[1], c);
+            }
+        }
+        __syncthreads();  // the arrays above are complete
         const int nb = min(kPlanThreads, p.batch - b0);
         for (long long i = me; i < tile_page; i += all) {
             const int s = upper(s_page, nb, i);
@@ -160,8 +165,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
         p.positions[i] = 0;
     }
     if (me == 0) {
-        p.counts[0] = int(taken);
-        p.counts[1] = int(placed);
+        p.counts[0] = int(s_sum[0]);  // the loop's last barrier is behind them
+        p.counts[1] = int(s_sum[1]);
     }
 }
 

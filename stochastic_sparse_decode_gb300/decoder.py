@@ -31,14 +31,6 @@ def _fits(t, dtypes, shape, dev) -> bool:
     return t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev
 
 
-def _rows_fit(t) -> bool:
-    """A [tokens][heads][d] tensor whose rows of heads x d elements are whole; tokens may lie apart."""
-    if t.is_contiguous():
-        return True
-    s, n = t.stride(), t.shape
-    return s[2] == 1 and (n[1] == 1 or s[1] == n[2]) and (n[0] == 1 or s[0] >= n[1] * n[2])
-
-
 def rope_table(max_pos, rot_dim, theta=10000.0, device="cuda") -> torch.Tensor:
     """cos_sin of santa_norm_rope, [max_pos][rot_dim] float32: angles n * theta^(-2i / rot_dim),
     formed in double precision (in single, the angle of position 100000 is off by 0.004)."""
@@ -157,16 +149,16 @@ class Decoder:
         self._pref = ctypes.byref(p)
         self._windows = {}
 
-    def _refuse(self, name, t, dtypes, shape, dev, rows=False):
-        """Says why a tensor that the C call would misread is refused: dtype, shape (None: any size), layout
-        (`rows`: [tokens][heads][d] whose tokens may lie apart), device."""
+    def _refuse(self, name, t, dtypes, shape, dev, how=""):
+        """Says why a tensor that the C call would misread is refused: dtype, shape (None: any size), device,
+        layout."""
         if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
             raise ValueError(f"{name}: a tensor of {' or '.join(sorted(map(str, dtypes)))} is needed")
         if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
             raise ValueError(f"{name}: shape {tuple(t.shape)}, needed {shape}")
-        if not (t.is_contiguous() or (rows and _rows_fit(t))):
-            raise ValueError(f"{name}: not contiguous")
-        raise ValueError(f"{name}: on {t.device}, needed on CUDA device {'of the other tensors' if dev >= 0 else 'memory'}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, not with the other tensors")
+        raise ValueError(f"{name}: not contiguous {how}".rstrip())
 
     def _stream(self, dev, stream):
         """The raw stream of a call whose tensors are on device `dev`, which must be the current one."""
@@ -266,10 +258,14 @@ class Decoder:
 
     def _rows(self, name, t, n, heads, dev):
         """(address, elements from token to token) of [tokens][heads][d], whose tokens may lie apart."""
-        shape = (n, heads, self.problem.head_dim)
-        if t.dtype not in self._dt or t.shape != shape or t.get_device() != dev or not _rows_fit(t):
-            self._refuse(name, t, self._dt, shape, dev, rows=True)
-        return t.data_ptr(), t.stride(0) if n > 1 else heads * shape[2]
+        d = self.problem.head_dim
+        if t.dtype in self._dt and t.shape == (n, heads, d) and t.get_device() == dev:
+            if t.is_contiguous():
+                return t.data_ptr(), heads * d
+            s = t.stride()
+            if s[2] == 1 and (s[1] == d or heads == 1) and (n == 1 or s[0] >= heads * d):
+                return t.data_ptr(), s[0] if n > 1 else heads * d
+        self._refuse(name, t, self._dt, (n, heads, d), dev, "row by row ")
 
     def kv4_append(self, k, v, slot_map, kv4, debug=None, stream=None) -> torch.Tensor:
         """Stores tokens k, v [tokens][Hkv][d] into rows slot_map of the 4-bit cache (santa_kv4_append)."""
