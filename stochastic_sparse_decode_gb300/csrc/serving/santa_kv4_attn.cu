@@ -7,8 +7,8 @@
 //   sum_j e_j v_j = sum_j (e_j s_jg) c_j    + sum_j e_j m'_jg         (group by group),
 // and both large products run on the tensor cores (fp16 mma m16n8k16).  Two codes become an
 // fp16 pair by two instructions: masked out of the word into the low bits of 1024 (one LOP3),
-// then 1024 + n - 1032, or (1024 + 16 n) / 16 - 72 for the high nibble of a byte (one HFMA2),
-// both exact.  The centring is not for looks: with n itself the two terms of the second line
+// then 1024 + n - 1032, or 1024 + 16 n - 1152 for the high nibble of a byte (one HADD2), both
+// exact; the factor of 16 goes into q and into the last product.  The centring is not for looks: with n itself the two terms of the second line
 // are each about 2.6 standard deviations of the values and cancel to the mean of thousands
 // of them, so that the last bits of the tensor cores' truncating sums showed as 3e-4 of the
 // output at 32768 keys; and codes used as they lie in memory, as fp16 subnormals n 2^-24 (no
@@ -81,18 +81,22 @@ __device__ __forceinline__ int exponent(float x) {
     return e < -100 ? -100 : e > 100 ? 100 : e;
 }
 
-// The low (or high) nibbles of bytes 0 and 2 of w, less 8, as an fp16 pair.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
-    const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + n: the last bit of 1024 in fp16 is 1
-    const __half2 c = __hadd2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0xe408)));  // -1032
-    return *reinterpret_cast<const uint32_t *>(&c);
+// (w & mask) | 0x6400 twice: codes on top of 1024 in fp16, whose last bits count ones.  As PTX,
+// because the compiler spends two instructions on the expression (128 more per block).
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t on_1024(uint32_t w) {
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "n"(kMask), "r"(0x64006400u));
+    return x;
 }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-    const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
-    const __half2 c = __hfma2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x2c00)),
-                              __half2half2(__ushort_as_half(0xd480)));  // / 16 - 72
-    return *reinterpret_cast<const uint32_t *>(&c);
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
+// The low nibbles of bytes 0 and 2 of w less 8, as an fp16 pair; the high nibbles less 8, times 16.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return add_half2(on_1024<0x000f000fu>(w), 0xe408e408u); }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return add_half2(on_1024<0x00f000f0u>(w), 0xe480e480u); }
 
 template <int D, typename Q, int GT>
 struct Kv4Geom {
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 
     // State of the heads of columns 2t, 2t + 1: M, the shares of the lane's own keys of Z and of
     // the sums of e_j m'_jg, and O^T: tile (word i of the lane's V words, q) holds elements 2q
-    // (O[..][0 .. 1]) and 2q + 1 (O[..][2 .. 3]) of word (kW / 2) g + i, times fscale.
+    // (O[..][0 .. 1]) and 2q + 1 (O[..][2 .. 3]) of word (kW / 2) g + i, times fscale and 16 fscale.
     const int h0 = kTwice ? 2 * (t & 1) : 2 * t;  // head of column 2t
     float M[2], Z[2], base[kG][2], O[kTiles][4], fscale;
     auto reset = [&]() {
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) O[n][j] += __shfl_xor_sync(kFull, O[n][j], 2);
         }
-        const float f = 1.f / fscale;  // a power of two
+        const float f0 = 1.f / fscale, f1 = 0.0625f / fscale;  // powers of two
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int h = h0 + j;
@@ -254,8 +258,8 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) {
                     const int i = n / 4, at = 8 * (kW / 2 * g + i) + 2 * (n % 4);
-                    *reinterpret_cast<float2 *>(dst + at) = make_float2(fmaf(O[n][j], f, base[i % kG][j]) * inv,
-                                                                        fmaf(O[n][2 + j], f, base[i % kG][j]) * inv);
+                    *reinterpret_cast<float2 *>(dst + at) = make_float2(fmaf(O[n][j], f0, base[i % kG][j]) * inv,
+                                                                        fmaf(O[n][2 + j], f1, base[i % kG][j]) * inv);
                 }
                 if (!final && g == 0) {
                     sh.M[slot][h] = M[j];
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             if (fresh) {
                 fresh = false;
                 // q as the B operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
-                // words kW t + u of the head of column g
+                // words kW t + u of the head of column g, the latter / 16 because their codes are high nibbles
                 const int hg = kTwice ? g & 3 : g;
                 const Q *qh = static_cast<const Q *>(p.q) +
                               (size_t(w.heads[sel].b) * p.Hq + w.heads[sel].kvh * G + min(hg, G - 1)) * D + t * kW * 8;
@@ -333,12 +337,12 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     for (int i = 0; i < kG; ++i) sum[i] += __shfl_xor_sync(kFull, sum[i], s);
                 }
                 const int e = exponent(mx);
-                const float f = pow2(14 - e);
+                const float f = pow2(14 - e), fh = f * 0.0625f;
 #pragma unroll
                 for (int u = 0; u < kW; ++u) {
                     float a[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * f;
+                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * (i & 1 ? fh : f);
 #pragma unroll
                     for (int part = 0; part < kQ; ++part)
 #pragma unroll
