@@ -1,23 +1,28 @@
 // santa_kv4_attn.cu -- exact decode attention over a K/V cache held in 4 bits.
 //
 // A key row stands for k_i = m_g + s_g n_i (codes n_i in 0 .. 15; scale s_g and minimum m_g
-// of element i's group g), a value row likewise.  With the codes centred, c = n - 8, and
-// m' = m + 8 s,
-//   q . k_j       = sum_g s_jg (q_g . c_jg) + m'_jg sum(q_g)
-//   sum_j e_j v_j = sum_j (e_j s_jg) c_j    + sum_j e_j m'_jg         (group by group),
-// and both large products run on the tensor cores (fp16 mma m16n8k16).  Two codes become an
-// fp16 pair by two instructions: masked out of the word into the low bits of 1024 (one LOP3),
-// then 1024 + n - 1032, or 1024 + 16 n - 1152 for the high nibble of a byte (one HADD2), both
-// exact; the factor of 16 goes into q and into the last product.  The centring is not for looks: with n itself the two terms of the second line
-// are each about 2.6 standard deviations of the values and cancel to the mean of thousands
-// of them, so that the last bits of the tensor cores' truncating sums showed as 3e-4 of the
-// output at 32768 keys; and codes used as they lie in memory, as fp16 subnormals n 2^-24 (no
-// second instruction), lose up to ten bits when products are aligned by their operands'
-// exponents.
+// of element i's group g), a value row likewise, so that group by group
+//   q . k_j       = sum_g s_jg (q_g . n_jg)       + m_jg sum(q_g)
+//   sum_j e_j v_j = sum_j (e_j s_jg) (n_j - 8)    + sum_j e_j (m_jg + 8 s_jg)
+// and both large products run on the tensor cores (fp16 mma m16n8k16).
+//
+// K's codes go in as they lie in memory: masked out of its word a code is, as an fp16 bit
+// pattern, the subnormal n 2^-24 (low nibble of a byte) or n 2^-20 (high nibble); the powers
+// of two go into q and the logits' factor.  V's codes are centred, two by one LOP3 (masked
+// onto the low bits of 1024) and one exact add (1024 + n - 1032, or 1024 + 16 n - 1152).  The
+// centring is not for looks: with n itself the two terms of the second line are each about
+// 2.6 standard deviations of the values and cancel to the mean of thousands of them, and
+// what the tensor cores truncate showed as 3e-4 of the output at 32768 keys, all the more as
+// subnormals (products are aligned by their operands' exponents, up to ten bits above their
+// own).  Errors of the logits are independent from key to key and average out: 2.3e-7 of the
+// output at 8000 keys with K centred, 4.8e-7 as it is, for 64 instructions less per block
+// (16 x 32768 keys: 146 -> 139 us).
+//
 // Codes are the A operand of both (rows: keys, then elements), queries and weights the B
 // operand (columns: heads).  A word of K's codes gives a lane the A fragments of two products
-// (1 shift besides); two keys' words of V, paired by byte permutes, those of eight.  The weights turn from the layout in which the logits come out
-// into the one in which they go in by movmatrix.
+// (4 ands, 1 shift); two keys' words of V, paired by byte permutes, those of eight.  The
+// weights turn from the layout in which the logits come out into the one in which they go in
+// by movmatrix.
 //
 // Precision: q is scaled by a power of two per head to fit fp16 (a bf16 q is exact so; an
 // fp32 q is taken in two parts, 22 bits); the weights e_j s_jg likewise in two parts, under a
@@ -94,9 +99,10 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // nibbles of bytes 0 and 2
 // The low nibbles of bytes 0 and 2 of w less 8, as an fp16 pair; the high nibbles less 8, times 16.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return add_half2(on_1024<0x000f000fu>(w), 0xe408e408u); }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return add_half2(on_1024<0x00f000f0u>(w), 0xe480e480u); }
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return add_half2(on_1024<kLow>(w), 0xe408e408u); }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) { return add_half2(on_1024<kHigh>(w), 0xe480e480u); }
 
 template <int D, typename Q, int GT>
 struct Kv4Geom {
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
     };
 
     // State of the heads of columns 2t, 2t + 1: M, the shares of the lane's own keys of Z and of
-    // the sums of e_j m'_jg, and O^T: tile (word i of the lane's V words, q) holds elements 2q
+    // the sums of e_j (m + 8 s), and O^T: tile (word i of the lane's V words, q) holds elements 2q
     // (O[..][0 .. 1]) and 2q + 1 (O[..][2 .. 3]) of word (kW / 2) g + i, times fscale and 16 fscale.
     const int h0 = kTwice ? 2 * (t & 1) : 2 * t;  // head of column 2t
     float M[2], Z[2], base[kG][2], O[kTiles][4], fscale;
@@ -348,14 +354,14 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) qf[part][u][i] = half_pair(a[i], a[i + 4]);
                 }
-                // y = sum_g s_g c_g + m'_g sum(q_g) / 2^(e - 14), in the products' units
+                // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)), in the products' units
                 const int e0 = __shfl_sync(kFull, e, 4 * h0), e1 = __shfl_sync(kFull, e, 4 * (h0 + 1));
                 const float scale2 = p.scale * 1.4426950408889634f;
-                kq = make_float2(pow2(e0 - 14) * scale2, pow2(e1 - 14) * scale2);
+                kq = make_float2(pow2(e0 + 10) * scale2, pow2(e1 + 10) * scale2);
 #pragma unroll
                 for (int i = 0; i < kG; ++i)
-                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(14 - e0),
-                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(14 - e1));
+                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(-10 - e0),
+                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(-10 - e1));
             }
             if constexpr (kTma) {
                 if (!mbar_wait(&bars[cur], phase >> cur & 1)) {
@@ -383,12 +389,12 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     fscale = f;
                 }
                 if (!kTma && more) load_par(next, next_seen);
-                // per key and group (s, s, m', m') of K, then of V; the slots of a key turn with the key
+                // per key and group (s, s, m, m) of K, then (s, s, m + 8 s, twice) of V; the slots of a key turn with the key
                 // against bank conflicts
 #pragma unroll
                 for (int i = 0; i < 2 * kG; ++i) {
                     const float sc = i < kG ? sm[i].x : sm[i].x * fscale;
-                    const float mid = fmaf(8.f, sm[i].x, sm[i].y);
+                    const float mid = i < kG ? sm[i].y : fmaf(8.f, sm[i].x, sm[i].y);  // V: m + 8 s
                     par[lane * 2 * kG + ((i + lane) & (2 * kG - 1))] = make_float4(sc, sc, mid, mid);
                 }
                 __syncwarp();
@@ -412,10 +418,10 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                         for (int part = kQ - 1; part >= 0; --part) {
                             if (u < kG && s == 0 && part == kQ - 1)
-                                mma_f16_zero(c[u % kG], low_codes(a), low_codes(b), high_codes(a), high_codes(b), qf[part][u][2 * s],
+                                mma_f16_zero(c[u % kG], a & kLow, b & kLow, a & kHigh, b & kHigh, qf[part][u][2 * s],
                                              qf[part][u][2 * s + 1]);
                             else
-                                mma_f16(c[u % kG], low_codes(a), low_codes(b), high_codes(a), high_codes(b), qf[part][u][2 * s],
+                                mma_f16(c[u % kG], a & kLow, b & kLow, a & kHigh, b & kHigh, qf[part][u][2 * s],
                                         qf[part][u][2 * s + 1]);
                         }
                     }
@@ -520,8 +526,9 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                                     mma_f16(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks], b[2 * ks + 1]);
                             }
                         float(&o)[4] = O[4 * i + 2 * half + s];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[j] = fmaf(o[j], j & 1 ? sco.y : sco.x, acc[j]);
+                        const float2 lo = __ffma2_rn(make_float2(o[0], o[1]), sco, make_float2(acc[0], acc[1]));
+                        const float2 hi = __ffma2_rn(make_float2(o[2], o[3]), sco, make_float2(acc[2], acc[3]));
+                        o[0] = lo.x, o[1] = lo.y, o[2] = hi.x, o[3] = hi.y;
                     }
                 }
             if (!kTma && more) load_v(next, next_seen);
