@@ -14,10 +14,11 @@
 // than 1e-5 from the middle between two codes rounds as the quotient does.
 //
 // A prompt of 8191 tokens, 8 heads of 128, is 43 MB in and out for either direction (6.3 us at
-// the copy rate), and both were bound by instructions (295 and 149 per warp and row: 22 us
-// each).  What brought them down: one division per lane instead of one per row (a lane keeps
-// its head and steps through tokens), packed minimum and maximum, no IEEE division, rounding
-// and packing by the low bits of a large float, and codes read as fp16 subnormals.
+// the copy rate).  Both are bound by instructions (211 and 110 per warp and row at first 295 and
+// 149): 29 us for the two, at first 44.  What brought them down: one division per lane instead
+// of one per row (a lane keeps its head and steps through tokens), packed minimum and maximum,
+// no IEEE division, rounding and packing by the low bits of a large float, and codes read as
+// fp16 subnormals.  One to four rows in flight per lane: 31.1, 29.6, 31.0, 31.3 us.
 #include <cuda_fp16.h>
 
 #include "santa_rows.cuh"
@@ -28,7 +29,7 @@ namespace santa {
 namespace {
 
 constexpr int kStoreThreads = 256;
-constexpr int kMany = 2;
+constexpr int kMany = 2;  // rows of a lane in flight
 constexpr float kHalfMax = 65504.f;
 
 // The rows of a token are K of its KV heads, then V.  A lane row (D / 8 lanes) takes row

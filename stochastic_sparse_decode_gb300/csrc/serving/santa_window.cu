@@ -19,6 +19,12 @@
 // leave 2^-17 per weight, which shows in the fp32 output), transposed in registers
 // (movmatrix), and each block's sums start from zero and are added to O by an fp32 fma:
 // the tensor cores' additions truncate, and a chain over thousands of keys would drift.
+//
+// Bound by memory where there is enough of it: 64 ragged sequences of 4096 to 32768 tokens,
+// window 4096 and 4 sinks (1.07 GB of K and V), 176 us = 6.1 TB/s, 0.90 of the copy rate; 12
+// warps with one K and one V buffer each keep 196 KB in flight per SM.  One sequence (16.8 MB)
+// takes 10.9 us, a chain of dependent steps: lengths and plan 1.5 us, first K and V 1.5,
+// weights and sums 1, join within the CTA 1, count 1.5, parts 2 (device timestamps).
 // fp32: a lane forms the whole dot products of one key (rows read along the swizzle
 // without bank conflicts), then owns d / 32 dimensions of the sums.
 #include "santa_split.cuh"
