@@ -440,7 +440,7 @@ enum {
  *   kv_lens, new_lens  device [batch] int32
  *   page_table         device [batch][max_pages] int32, updated in place
  *   free_pages         device [num_free] int32, distinct pages no sequence holds
- *   slot_map           device [max_tokens] int64: row of each new token, the tokens
+ *   slot_map           device [max_tokens] int64 (16-byte aligned, as positions): row of each new token, the tokens
  *                      of sequence 0 first, then those of sequence 1, ...
  *   positions          device [max_tokens] int32: their positions
  *   lens_out           device [batch] int32: the new lengths; not kv_lens itself
@@ -512,6 +512,7 @@ typedef struct {
  * empty sequence gives zeros.  Results do not depend on timing: equal calls give
  * equal bits.  What the visible keys and values hold must be finite (else a head's
  * output may be NaN where a plain sum would be infinite).
+ * Supported while batch * Hkv * max_len / 32 stays below 10^12.
  * Workspace: santa_split_workspace_size, prepared once by santa_split_workspace_init;
  * every call leaves it ready for the next, of santa_decode_window or santa_decode_kv4
  * on the same problem, and calls that may overlap (two graphs, two streams) need one

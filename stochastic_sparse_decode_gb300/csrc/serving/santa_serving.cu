@@ -37,6 +37,8 @@ int check_split(const santa_problem *p) {
     if (p->batch < 0 || p->batch > 65535 || p->max_len < 0) return SANTA_INVALID_ARG;
     if (p->num_q_heads % p->num_kv_heads != 0) return SANTA_INVALID_ARG;
     if (p->num_q_heads / p->num_kv_heads > kMaxGroup) return SANTA_UNSUPPORTED;
+    // a warp counts its blocks of 32 keys in 31 bits
+    if (double(p->batch) * p->num_kv_heads * (p->max_len / 32 + 2) > 1e12) return SANTA_UNSUPPORTED;
     return SANTA_OK;
 }
 // Rows of `heads` vectors of d elements, `stride` elements apart.

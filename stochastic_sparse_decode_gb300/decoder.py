@@ -175,11 +175,22 @@ class Decoder:
         return out
 
     def split_workspace(self) -> torch.Tensor:
-        """The workspace of window and kv4 calls (kept; calls that overlap need a Decoder each)."""
+        """The workspace of window and kv4 calls (kept; calls that overlap need a Decoder each).  The first use
+        prepares it, which a stream capture would only record: call this before capturing."""
         if "split" not in self._ws:
-            # zero-filled: what santa_split_workspace_init does
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the workspace must exist before a capture: call split_workspace() first")
+            # zero-filled: what santa_split_workspace_init does; complete before a call on any stream
             self._ws["split"] = torch.zeros(split_workspace_size(self.problem), dtype=torch.uint8, device=self.device)
+            torch.cuda.current_stream(self._ws["split"].device).synchronize()
         return self._ws["split"]
+
+    def _window(self, window, sinks):
+        if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+            raise ValueError(f"window {window}, sinks {sinks}: whole numbers from 0 to 2^31 - 1 are needed")
+        if len(self._windows) >= 64:
+            self._windows.clear()
+        return self._windows.setdefault((window, sinks), ctypes.byref(Window(window, sinks)))
 
     def _attend(self, kind, q, k, v, kv_indptr, pages, window, sinks, out, debug, stream):
         dev = q.get_device()
@@ -209,10 +220,12 @@ class Decoder:
         out = self._out(out, dev)
         w = self._windows.get((window, sinks))
         if w is None:
-            w = self._windows[(window, sinks)] = ctypes.byref(Window(window, sinks))
+            w = self._window(window, sinks)
         ws = self._ws.get("split")
         if ws is None:
             ws = self.split_workspace()
+        if ws.get_device() != dev:
+            raise ValueError(f"the tensors are on CUDA device {dev}, this Decoder's workspace on {ws.device}")
         st = self._stream(dev, stream)
         dbg = None if debug is None else ctypes.byref(debug)
         L = lib()

@@ -804,6 +804,84 @@ def test_two_streams_with_a_workspace_each(kind):
         assert torch.equal(got, c["out"])
 
 
+def test_c_entry_points_by_name():
+    """The functions that carry the C names give what the Decoder's methods give: a caller's own workspace,
+    prepared by santa_split_workspace_init and full of garbage before; no window given to the 4-bit call."""
+    c = _attention_case("window", "bf16", 128, 2, 4, [4000, 0, 77], 0, 0, 0, seed=41)
+    dec, q, (k, v), ind = c["dec"], c["q"], c["pools"], c["addr"]["indptr"]
+    p = dec.problem
+    n = 6
+    ws = torch.full((sd.split_workspace_size(p),), 0xFF, dtype=torch.uint8, device="cuda")
+    sd.santa_split_workspace_init(p, ws)
+    out = torch.empty_like(c["out"])
+    sd.santa_decode_window(p, sd.Window(100, 3), q, k, v, ind, out, ws)
+    assert torch.equal(out, dec.window(q, k, v, ind, 100, 3))
+    slots = torch.randperm(p.total_tokens, device="cuda")[:n].contiguous()
+    caches = [torch.zeros((p.total_tokens, 2, 144), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    assert sd.kv4_size(p) == caches[0].numel()
+    x = torch.randn((n, 12, 128), device="cuda").bfloat16()
+    sd.santa_kv4_append(p, x[:, 8:10], x[:, 10:], slots, caches[0])
+    dec.kv4_append(x[:, 8:10], x[:, 10:], slots, caches[1])
+    assert torch.equal(*caches)
+    a, b = (torch.empty((n, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    sd.santa_kv4_read(p, n, caches[0], slots, a, b)
+    assert all(torch.equal(s, t) for s, t in zip((a, b), dec.kv4_read(caches[0], slots)))
+    sd.santa_kv4_read(p, n, caches[0], None, None, b)  # rows 0 .. n - 1, V alone
+    assert torch.equal(b, dec.kv4_read(caches[0], torch.arange(n, device="cuda"))[1])
+    sd.santa_decode_kv4(p, None, q, caches[0], ind, out, ws)
+    assert torch.equal(out, dec.kv4(q, caches[0], ind))
+    cs, pos = rope_table(50, 64), torch.arange(n, dtype=torch.int32, device="cuda")
+    w = torch.rand(128, device="cuda").bfloat16()
+    rope = sd.Rope(w.data_ptr(), None, 1e-6, cs.data_ptr(), 50, 64, 0)  # norms of the queries alone
+    kc, vc, kd, vd = (torch.zeros_like(k) for _ in range(4))
+    qo = torch.empty((n, 8, 128), dtype=torch.bfloat16, device="cuda")
+    sd.santa_norm_rope(p, rope, x[:, :8], x[:, 8:10], x[:, 10:], pos, slots, qo, kc, vc)
+    assert torch.equal(qo, dec.norm_rope(x[:, :8], x[:, 8:10], x[:, 10:], pos, slots, cs, kd, vd, q_weight=w))
+    assert torch.equal(kc, kd) and torch.equal(vc, vd)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, new, table = torch.tensor([3, 40], **i32), torch.tensor([1, 30], **i32), torch.tensor([[5, 0, 0], [2, 3, 0]], **i32)
+    free, slot_map, positions = torch.tensor([7, 1], **i32), torch.empty(33, dtype=torch.int64, device="cuda"), torch.empty(33, **i32)
+    lens_out, counts = torch.empty(2, **i32), torch.empty(2, **i32)
+    sd.santa_page_plan(32, 9, lens, new, table, free, slot_map, positions, lens_out, counts)
+    assert counts.tolist() == [1, 31] and table.tolist() == [[5, 0, 0], [2, 3, 7]] and lens_out.tolist() == [4, 70]
+    assert slot_map[:3].tolist() == [163, 104, 105] and slot_map[-3:].tolist() == [229, -1, -1]
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_workspace_before_capture_and_windows_in_range(kind):
+    """A Decoder whose first call would be captured is refused (its workspace would only be zeroed by a replay);
+    windows beyond 31 bits are refused, not cut; a call on another stream finds the workspace prepared."""
+    c = _attention_case(kind, "bf16", 128, 2, 4, [5000, 7], 0, 0, 0, seed=40)
+    p = c["dec"].problem
+    fresh = Decoder(p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim, p.total_tokens, p.max_len, 256, 1, "bf16")
+    out = torch.empty_like(c["out"])
+    call = lambda dec, w=0, s=0, **kw: _run_attention(kind, dec, c["q"], c["pools"], c["addr"], 0, w, s, out=out)  # noqa: E731
+    with pytest.raises(RuntimeError, match="before a capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            call(fresh)
+    torch.cuda.synchronize()
+    for w, s in ((-1, 0), (2**31, 0), (0, 2**32 + 5)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(fresh, w, s)
+    junk = torch.full((1 << 26,), 7, dtype=torch.uint8, device="cuda")  # what a fresh allocation may hold
+    del junk
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    if kind == "window":
+        fresh.window(c["q"], *c["pools"], c["addr"]["indptr"], 0, out=out, stream=side)
+    else:
+        fresh.kv4(c["q"], c["pools"][0], c["addr"]["indptr"], out=out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, c["out"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(fresh)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, c["out"])
+
+
 def test_rows_beyond_32_bit_offsets():
     """A cache of more than 2^32 bytes (and 2^31 elements of a 4-bit one): the last rows are found."""
     hkv, d = 8, 128

@@ -97,6 +97,8 @@ def test_attention_refuses(sd, name):
     assert f(ws_bytes=100) == sd.WORKSPACE_TOO_SMALL
     assert f(p=_problem(sd, head_dim=32)) == sd.UNSUPPORTED
     assert f(p=_problem(sd, num_q_heads=18)) == sd.UNSUPPORTED  # 9 query heads per KV head
+    huge = dict(batch=65535, num_q_heads=8, num_kv_heads=8, max_len=2**31 - 1)
+    assert f(p=_problem(sd, **huge)) == sd.UNSUPPORTED  # more blocks than a warp counts
     assert f(p=_problem(sd, batch=0)) == sd.OK
     if name == "santa_decode_window":
         assert f(window=None) == sd.INVALID_ARG
