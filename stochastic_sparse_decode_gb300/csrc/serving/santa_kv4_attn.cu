@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                 const uint4 x = *reinterpret_cast<const uint4 *>(src);
                 kc[o][0] = x.x, kc[o][1] = x.y, kc[o][kW - 2] = x.z, kc[o][kW - 1] = x.w;
             } else {
-                const uint2 x = seen >> (8 * o + g) & 1 ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
+                const uint2 x = seen >> (8 * o + g) & 1 ? load(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
                 kc[o][0] = x.x, kc[o][1] = x.y;
             }
             src += 8 * step;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     const uint2 x = *reinterpret_cast<const uint2 *>(at);
                     vc[o][i][0] = x.x, vc[o][i][kW / 2 - 1] = x.y;
                 } else {
-                    vc[o][i][0] = seen >> (8 * o + 2 * t + i) & 1 ? __ldg(reinterpret_cast<const uint32_t *>(at)) : 0u;
+                    vc[o][i][0] = seen >> (8 * o + 2 * t + i) & 1 ? load(reinterpret_cast<const uint32_t *>(at)) : 0u;
                 }
             }
             src += 8 * step;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             const uint4 x = in ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
             pc[0] = x.x, pc[1] = x.y, pc[2 * kG - 2] = x.z, pc[2 * kG - 1] = x.w;
         } else {
-            const uint2 x = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
+            const uint2 x = in ? load(reinterpret_cast<const uint2 *>(src)) : make_uint2(0, 0);
             pc[0] = x.x, pc[1] = x.y;
         }
     };
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) {
                         float2 pr[Vec16<Q>::kPairs];
-                        Vec16<Q>::unpack(__ldg(reinterpret_cast<const uint4 *>(qh + 8 * u) + i), pr);
+                        Vec16<Q>::unpack(load(reinterpret_cast<const uint4 *>(qh + 8 * u) + i), pr);
 #pragma unroll
                         for (int j = 0; j < Vec16<Q>::kPairs; ++j) {
                             x[u][2 * (i * Vec16<Q>::kPairs + j)] = pr[j].x;

@@ -51,7 +51,7 @@ __device__ __forceinline__ RowOf row_of(const StoreParams &p, int lanes) {
 // The token's slot, -1 if it has none (padding, behind the last token, or beyond the cache: flagged).
 __device__ __forceinline__ long long slot_of(const StoreParams &p, const RowOf &r) {
     if (!r.live) return -1;
-    const long long slot = p.slot_map ? __ldg(p.slot_map + r.t) : r.t;
+    const long long slot = p.slot_map ? load(p.slot_map + r.t) : r.t;
     if (slot >= p.total_tokens) {
         if (p.err) atomicOr(p.err, SANTA_ERR_SLOT);
         return -1;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StorePa
     for (int b = 0; b < 2; ++b) {
 #pragma unroll
         for (int i = 0; i < int(sizeof(T)) / 2; ++i)
-            raw[b][i] = __ldg(reinterpret_cast<const uint4 *>(src + b * 8 * kL) + i);
+            raw[b][i] = load(reinterpret_cast<const uint4 *>(src + b * 8 * kL) + i);
         Elems8<T>::unpack(raw[b], x[b]);
     }
     float2 ex = extremes<kGroups, kL>(raw, x, T());
@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StorePara
     if (slot >= 0) {
         const unsigned char *rec = p.kv4 + ((size_t)slot * p.Hkv + r.h) * kv4_record(D);
         const uint32_t *words = reinterpret_cast<const uint32_t *>(rec + r.which * (D / 2)) + l;
-        word[0] = __ldg(words);
-        word[1] = __ldg(words + kL);
-        pair = __ldg(reinterpret_cast<const uint32_t *>(rec + D + r.which * (D / 16)) + l % kGroups);
+        word[0] = load(words);
+        word[1] = load(words + kL);
+        pair = load(reinterpret_cast<const uint32_t *>(rec + D + r.which * (D / 16)) + l % kGroups);
     }
     const float2 sm = __half22float2(*reinterpret_cast<const __half2 *>(&pair));
     // codes as fp16 subnormals, n 2^-24 and n 2^-20: the products with the scale stay exact

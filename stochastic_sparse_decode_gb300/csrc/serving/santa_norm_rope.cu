@@ -40,8 +40,8 @@ __device__ __forceinline__ void take_rows(const T *src, T *dst, const T *weight,
     float w[8];
     if (kQK && weight) {
         float u[4], v[4];
-        E::unpack(__ldg(reinterpret_cast<const Raw *>(weight + a0)), u);
-        E::unpack(__ldg(reinterpret_cast<const Raw *>(weight + a1)), v);
+        E::unpack(load(reinterpret_cast<const Raw *>(weight + a0)), u);
+        E::unpack(load(reinterpret_cast<const Raw *>(weight + a1)), v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = u[j], w[4 + j] = v[j];
     }
@@ -51,8 +51,8 @@ __device__ __forceinline__ void take_rows(const T *src, T *dst, const T *weight,
         for (int k = 0; k < kAhead; ++k) {
             const int r = base + part + k * parts;
             const T *at = src + min(r, end - 1) * D;
-            ra[k] = __ldg(reinterpret_cast<const Raw *>(at + a0));
-            rb[k] = __ldg(reinterpret_cast<const Raw *>(at + a1));
+            ra[k] = load(reinterpret_cast<const Raw *>(at + a0));
+            rb[k] = load(reinterpret_cast<const Raw *>(at + a1));
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
     pdl_wait();
     pdl_launch_dependents();
 
-    int pos = __ldg(p.positions + t);
+    int pos = load(p.positions + t);
     if (pos < 0 || pos >= p.max_pos) {
         if (p.err && live) atomicOr(p.err, SANTA_ERR_POSITION);
         pos = pos < 0 ? 0 : p.max_pos - 1;
     }
-    long long slot = p.slot_map ? __ldg(p.slot_map + t) : t;
+    long long slot = p.slot_map ? load(p.slot_map + t) : t;
     if (slot >= p.total_tokens) {
         if (p.err && live) atomicOr(p.err, SANTA_ERR_SLOT);
         slot = -1;
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
     float c[4] = {}, s[4] = {};
     if (turns) {
         const float *cs = p.cos_sin + (size_t)pos * p.rot_dim + 4 * l;
-        const float4 u = __ldg(reinterpret_cast<const float4 *>(cs));
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(cs + p.rot_dim / 2));
+        const float4 u = load(reinterpret_cast<const float4 *>(cs));
+        const float4 v = load(reinterpret_cast<const float4 *>(cs + p.rot_dim / 2));
         c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w;
         s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
     }

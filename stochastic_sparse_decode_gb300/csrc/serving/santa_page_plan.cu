@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
                 if (!s_ok[s]) continue;
                 pos[j] = s_len[s] + int(i - (s > 0 ? s_tok[s - 1] : 0));
                 const int pg = page_of(pos[j], p), fresh = pg - s_have[s];
-                const int id = fresh >= 0 ? __ldg(p.free_pages + page0 + (s > 0 ? s_page[s - 1] : 0) + fresh)
+                const int id = fresh >= 0 ? load(p.free_pages + page0 + (s > 0 ? s_page[s - 1] : 0) + fresh)
                                           : p.page_table[(size_t)(b0 + s) * p.max_pages + pg];
                 if (id >= 0 && id < p.num_pages)
                     slot[j] = (long long)id * p.page_size + pos[j] - pg * p.page_size;

@@ -138,7 +138,7 @@ __device__ __forceinline__ int page_row(const Params &p, int id) {
 // Loads the table's entry behind the page of w.key0, if the row has one.
 __device__ __forceinline__ void look_ahead(const Params &p, Walk &w, int b) {
     const int i = (w.key0 - w.in_page) / p.page_size + 1;
-    w.ahead = i < p.max_pages ? __ldg(p.page_table + (size_t)b * p.max_pages + i) : -1;
+    w.ahead = i < p.max_pages ? load(p.page_table + (size_t)b * p.max_pages + i) : -1;
 }
 // The run and the row of block w.n of h, by the page table.
 template <bool kPaged>
@@ -149,7 +149,7 @@ __device__ __forceinline__ void place(const SplitParams &sp, Walk &w, const Head
     if constexpr (kPaged) {
         const int page = w.key0 / p.page_size;
         w.in_page = w.key0 - page * p.page_size;
-        w.row = page_row(p, __ldg(p.page_table + (size_t)h.b * p.max_pages + page));
+        w.row = page_row(p, load(p.page_table + (size_t)h.b * p.max_pages + page));
         if (w.row >= 0) w.row += w.in_page;
         look_ahead(p, w, h.b);
     } else {

@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                     static_cast<const uint16_t *>(p.q) + (size_t(b) * p.Hq + kvh * G + min(g, G - 1)) * D);
 #pragma unroll
                 for (int ks = 0; ks < (kMma ? D / 16 : 1); ++ks) {
-                    qf[ks][0] = g < G ? __ldg(qh + 8 * ks + t) : 0u;
-                    qf[ks][1] = g < G ? __ldg(qh + 8 * ks + 4 + t) : 0u;
+                    qf[ks][0] = g < G ? load(qh + 8 * ks + t) : 0u;
+                    qf[ks][1] = g < G ? load(qh + 8 * ks + 4 + t) : 0u;
                 }
             }
             fresh = false;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                                                                             (((v & 7) ^ (lane & 7)) << 4));
 #pragma unroll
                         for (int h = 0; h < GT; ++h) {
-                            const float4 q4 = __ldg(reinterpret_cast<const float4 *>(qh + min(h, G - 1) * D) + v);
+                            const float4 q4 = load(reinterpret_cast<const float4 *>(qh + min(h, G - 1) * D) + v);
                             acc[h] = __ffma2_rn(make_float2(q4.x, q4.y), make_float2(k4.x, k4.y), acc[h]);
                             acc[h] = __ffma2_rn(make_float2(q4.z, q4.w), make_float2(k4.z, k4.w), acc[h]);
                         }
