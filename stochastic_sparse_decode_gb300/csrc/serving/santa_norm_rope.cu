@@ -13,8 +13,9 @@
 // Bound by memory: every row is read once and written once.  Lane rows take a token's rows in
 // turn (queries, then keys, then values), kMany of them in flight; when there are not enough
 // tokens to fill the GPU so, every lane row takes one row, and a warp passes by the kinds that
-// it has no row of (one row per lane at 8191 tokens: 54 us against 36; kMany at 777: 8.3 us
-// against 4.2).
+// it has no row of (one row per lane at 8191 tokens: 54 us; kMany at 777 tokens of 24 fp32 rows of
+// 64: 8.3 us against 3.1).  8191 tokens, 32 query and 8 KV heads of 128 in bf16, 206 MB: 35.4 us =
+// 5.8 TB/s, 0.85 of the copy rate.
 #include "santa_rows.cuh"
 #include "santa_serving.h"
 
@@ -108,7 +109,7 @@ __device__ __forceinline__ void take_rows(const T *src, T *dst, const T *weight,
 
 // A lane row takes the rows part, part + parts, ... of one token's Hq queries, Hkv keys and Hkv values.
 template <typename T, int D, bool kInter, int kAhead>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p, int parts) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_kernel(const RopeParams p, int parts) {
     constexpr int kL = D / 8;
     const int l = threadIdx.x % kL;
     const long long row = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / kL;
@@ -164,9 +165,12 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
 
 cudaError_t launch_norm_rope(const RopeParams &p, int dtype, int d, cudaStream_t stream) {
     const int rows = (p.q ? p.Hq : 0) + (p.k ? p.Hkv : 0) + (p.v ? p.Hkv : 0);
-    // lanes that fill the GPU once over (152 SMs of 2048 threads), within one to kMany rows in flight
+    // a third of the lanes that the SMs hold (2048 threads each): a lane row then pays for its
+    // table row and weights over more rows.  With all of them, 48 rows of 128 per token: 1000
+    // tokens 11.8 us instead of 7.0, 4000 21.8 instead of 18.9, 8191 36.1 instead of 35.4; with a
+    // sixth: 4000 tokens 24.8.
     int parts = 1;
-    while (parts < rows && (long long)p.tokens * parts * (d / 8) < 152LL * 2048) parts *= 2;
+    while (parts < rows && (long long)p.tokens * parts * (d / 8) < 152LL * 640) parts *= 2;
     const bool one = parts * kMany > rows;
     if (one) parts = rows;
     const long long threads = (long long)p.tokens * parts * (d / 8);
