@@ -309,10 +309,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             unsigned next_seen = 0;
             if (more) {
                 next_seen = seen_bits(w);
-                if constexpr (kTma)
-                    issue(cur ^ 1);  // read by the block before this one: every lane is past it
-                else
-                    next = record();
+                if constexpr (!kTma) next = record();
             }
             if (fresh) {
                 fresh = false;
@@ -377,6 +374,10 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     break;
                 }
                 phase ^= 1u << cur;
+                // the next block's buffer was read by the block before this one, which every lane is
+                // past.  Not before this block has landed: its copy would share the memory with the
+                // first blocks of all warps.
+                if (more) issue(cur ^ 1);
                 load_par(buf + cur * Geom::kBuf, seen);
                 load_k(buf + cur * Geom::kBuf, seen);
             }
@@ -557,9 +558,6 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                 raise_flag(p, SANTA_ERR_TIMEOUT | (5u << 8));
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&bars[cur], phase >> cur & 1) && clock64() - t0 < kWaitCycles) {
-                }
-                while (w.left > 0 && !mbar_try_wait(&bars[cur ^ 1], phase >> (cur ^ 1) & 1) &&
-                       clock64() - t0 < kWaitCycles) {
                 }
             }
             __syncwarp();
