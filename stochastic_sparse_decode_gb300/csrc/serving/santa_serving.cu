@@ -119,6 +119,7 @@ int attend(const santa_problem *p, const santa_window *w, const santa_pages *pag
     prm.err = err_word(dbg);
     sp.window = w && w->window > 0 && w->window < p->max_len ? w->window : p->max_len;
     sp.sinks = w ? w->sinks : 0;
+    sp.narrow = p->batch <= 128 && double(p->batch) * p->num_kv_heads * (p->max_len / 32 + 2) < 2147483648.0;
     sp.kv4 = static_cast<const unsigned char *>(kv4);
     sp.cnt = reinterpret_cast<unsigned int *>(ws);
     sp.part_mz = reinterpret_cast<float2 *>(ws + L.mz);

@@ -63,6 +63,7 @@ constexpr int kv4_record(int d) { return d + d / 8; }
 struct SplitParams {
     Params p;
     int window, sinks;         // window >= max_len: every key is visible
+    int narrow;                // at most 128 sequences whose units of 32 keys number below 2^31
     const unsigned char *kv4;  // 4-bit cache (k and v unused)
     unsigned int *cnt;         // [B][Hkv] CTAs that have stored a part of the head
     float2 *part_mz;           // [CTAs][2][G] (M, Z) of a CTA's first and last head, where others share it

@@ -197,9 +197,8 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         if ((int)blockIdx.x < ctas) take(X, stretch_start(X, ctas, blockIdx.x), stretch_start(X, ctas, blockIdx.x + 1));
     };
     Head h;
-    if (p.B <= 128) {  // every warp scans for itself: no barrier
-        int nb[4], len[4], from[4], most = 0;
-        long long end[4];
+    if (sp.narrow) {  // at most 128 sequences, units counted in 31 bits: every warp scans for itself, no barrier
+        int nb[4], len[4], from[4], end[4], most = 0, sum = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             nb[k] = len[k] = from[k] = 0;
@@ -217,55 +216,65 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                     empty &= empty - 1;
                     if (e % gridDim.x == blockIdx.x) zero_row(p, e);
                 }
-                long long v = nb[k];
+                int v = nb[k];
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     if (o >= p.B) break;
-                    const long long u = __shfl_up_sync(kFull, v, o);
+                    const int u = __shfl_up_sync(kFull, v, o);
                     if (lane >= o) v += u;
                 }
-                end[k] = total + v;
-                total = __shfl_sync(kFull, end[k], min(31, p.B - 32 * k - 1));
+                end[k] = sum + v;
+                sum = __shfl_sync(kFull, end[k], min(31, p.B - 32 * k - 1));
             }
         }
-        if (p.B * p.Hkv <= (int)gridDim.x &&
-            warp_max_int(most) <= kJoinUnits + divide(total * p.Hkv, int(gridDim.x))) {  // a CTA per head
-            ctas = p.B * p.Hkv;
-            if ((int)blockIdx.x < ctas) {
-                b = blockIdx.x / p.Hkv;
-                const int kvh = blockIdx.x - b * p.Hkv;
-                int n = 0;
-                long long e = 0;
+        const unsigned X = unsigned(sum) * p.Hkv, heads = unsigned(p.B) * p.Hkv;
+        unsigned cta0 = 0, size = 0;  // the CTA's stretch
+        if (heads <= gridDim.x && __reduce_max_sync(kFull, unsigned(most)) <= kJoinUnits + X / gridDim.x) {  // a CTA per head
+            ctas = int(heads);
+            if (blockIdx.x >= heads) return -1;
+            b = blockIdx.x / p.Hkv;
+            int e = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (b / 32 == k) {
-                        n = __shfl_sync(kFull, nb[k], b % 32);
-                        e = __shfl_sync(kFull, end[k], b % 32);
-                    }
-                if (n == 0) return -1;
-                const long long cta0 = (e - n) * p.Hkv + (long long)kvh * n;
-                take(total * p.Hkv, cta0, cta0 + n);
-            }
-        } else {
-            equal_stretches();
-        }
-        if ((int)blockIdx.x >= ctas) return -1;
-        if (w.left > 0) {
-#pragma unroll
-            for (int k = 3; k >= 0; --k)
-                if (32 * k < p.B) {
-                    const unsigned past = __ballot_sync(kFull, 32 * k + lane < p.B && end[k] * p.Hkv > x);
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        b = 32 * k + l;
-                        prefix = __shfl_sync(kFull, end[k] - nb[k], l);
-                        h.start = __shfl_sync(kFull, from[k], l);
-                        h.vis.L = __shfl_sync(kFull, len[k], l);
-                    }
+            for (int k = 0; k < 4; ++k)
+                if (b / 32 == k) {
+                    size = unsigned(__shfl_sync(kFull, nb[k], b % 32));
+                    e = __shfl_sync(kFull, end[k], b % 32);
                 }
-            h.b = b;
-            set_blocks(h, h.vis.L, sp);
+            if (size == 0) return -1;
+            cta0 = (unsigned(e) - size) * p.Hkv + (blockIdx.x - unsigned(b) * p.Hkv) * size;
+        } else {
+            const unsigned parts = min(gridDim.x, (X + kMinUnitsPerCta - 1) / kMinUnitsPerCta);
+            ctas = int(parts);
+            if (blockIdx.x >= parts) return -1;
+            const unsigned q = X / parts, r = X - q * parts;  // as stretch_start
+            cta0 = q * blockIdx.x + min(blockIdx.x, r);
+            size = q + (blockIdx.x < r ? 1 : 0);
         }
+        const unsigned q = size / NW, r = size - q * NW;
+        const unsigned at = cta0 + q * warp + min(unsigned(warp), r);
+        x = at;
+        w.left = int(q + (unsigned(warp) < r ? 1 : 0));
+        if (threadIdx.x == 0) {
+            sh.X = X;
+            sh.cta0 = cta0;
+            sh.cta1 = (long long)cta0 + size;
+            sh.ctas = ctas;
+        }
+        if (w.left <= 0) return 0;
+#pragma unroll
+        for (int k = 3; k >= 0; --k)
+            if (32 * k < p.B) {
+                const unsigned past = __ballot_sync(kFull, 32 * k + lane < p.B && unsigned(end[k]) * p.Hkv > at);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    b = 32 * k + l;
+                    prefix = __shfl_sync(kFull, end[k] - nb[k], l);
+                    h.start = __shfl_sync(kFull, from[k], l);
+                    h.vis.L = __shfl_sync(kFull, len[k], l);
+                }
+            }
+        h.b = b;
+        set_blocks(h, h.vis.L, sp);
     } else {
         constexpr int NT = NW * 32;
         auto block_scan = [&](long long v, long long *all) {
@@ -329,7 +338,7 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         w.left = 0;
         return 0;
     }
-    if (p.B > 128) load_head<kPaged>(h, sp, b);
+    if (!sp.narrow) load_head<kPaged>(h, sp, b);
     const long long rem = x - prefix * p.Hkv;
     h.kvh = int(divide(rem, h.nb));
     w.n = int(rem - (long long)h.kvh * h.nb);

@@ -439,6 +439,20 @@ def test_long_and_many(kind):
     _check_attention(_attention_case(kind, "f32", 64, 1, 2, [5000, 9000], 0, 0, 32, seed=3))
     rng = np.random.default_rng(4)
     _check_attention(_attention_case(kind, "bf16", 64, 1, 1, rng.integers(0, 50, 1100).tolist(), 20, 2, 32, seed=4))
+    # 40 and 128 sequences (two and four scans per warp), with long ones behind the first 32
+    _check_attention(_attention_case(kind, "bf16", 128, 2, 4, [3, 0] * 17 + [9000, 1, 0, 5000, 64, 2], 0, 0, 0, seed=5))
+    _check_attention(_attention_case(kind, "bf16", 64, 1, 2, rng.integers(0, 900, 128).tolist(), 0, 0, 32, seed=6))
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+def test_many_units_allowed_by_a_large_bound(kind):
+    """max_len far beyond the lengths: the count of units is then kept in 64 bits, by another path of the plan."""
+    for lens in ([5000, 0, 33, 700], [40], list(range(140))):
+        c = _attention_case(kind, "bf16", 128, 2, 4, lens, 600, 3, 0, seed=50)
+        p = c["dec"].problem
+        big = Decoder(p.batch, 8, 2, 128, p.total_tokens, 2**31 - 1, 256, 1, "bf16")
+        c["out"] = _run_attention(kind, big, c["q"], c["pools"], c["addr"], 0, 600, 3)
+        _check_attention(c)
 
 
 @pytest.mark.parametrize("kind", ["window", "kv4"])
