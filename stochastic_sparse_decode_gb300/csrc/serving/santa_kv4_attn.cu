@@ -6,21 +6,20 @@
 //   sum_j e_j v_j = sum_j (e_j s_jg) (n_j - 8)    + sum_j e_j (m_jg + 8 s_jg)
 // and both large products run on the tensor cores (fp16 mma m16n8k16).
 //
-// K's codes go in as they lie in memory: masked out of its word a code is, as an fp16 bit
-// pattern, the subnormal n 2^-24 (low nibble of a byte) or n 2^-20 (high nibble); the powers
-// of two go into q and the logits' factor.  V's codes are centred, two by one LOP3 (masked
-// onto the low bits of 1024) and one exact add (1024 + n - 1032, or 1024 + 16 n - 1152).  The
-// centring is not for looks: with n itself the two terms of the second line are each about
-// 2.6 standard deviations of the values and cancel to the mean of thousands of them, and
-// what the tensor cores truncate showed as 3e-4 of the output at 32768 keys, all the more as
-// subnormals (products are aligned by their operands' exponents, up to ten bits above their
-// own).  Errors of the logits are independent from key to key and average out: 2.3e-7 of the
-// output at 8000 keys with K centred, 4.8e-7 as it is, for 64 instructions less per block
-// (16 x 32768 keys: 146 -> 139 us).
+// K's codes need no conversion: shifted to bits 4 .. 7 and masked out of its word a code is,
+// as an fp16 bit pattern, the subnormal n 2^-20; the power of two goes into the logits'
+// factor.  V's codes are centred, two by one LOP3 (masked onto the low bits of 1024) and one
+// exact add (1024 + n - 1032, or 1024 + 16 n - 1152).  The centring is not for looks: with n
+// itself the two terms of the second line are each about 2.6 standard deviations of the values
+// and cancel to the mean of thousands of them, and what the tensor cores truncate showed as
+// 3e-4 of the output at 32768 keys, all the more as subnormals (products are aligned by their
+// operands' exponents, which a subnormal's value may lie far below).  Errors of the logits are
+// independent from key to key and average out; low nibbles left at bits 0 .. 3 (n 2^-24), two
+// shifts less per word, cost up to 1.2e-6 of the output of a few keys.
 //
 // Codes are the A operand of both (rows: keys, then elements), queries and weights the B
 // operand (columns: heads).  A word of K's codes gives a lane the A fragments of two products
-// (4 ands, 1 shift); two keys' words of V, paired by byte permutes, those of eight.  The
+// (3 shifts, 4 ands); two keys' words of V, paired by byte permutes, those of eight.  The
 // weights turn from the layout in which the logits come out into the one in which they go in
 // by movmatrix.
 //
@@ -39,13 +38,13 @@
 // d = 64: a record is 72 bytes, which TMA's strides cannot express; the codes go from global
 // memory to registers, the next block's while the current one is computed.
 //
-// Bound by instructions: 770 per warp and block of 32 keys (ALU pipe 320, FMA pipe 277, 32
-// products), 0.57 issued per cycle and scheduler by 4 warps of 128 registers.  16 sequences of
-// 32768 tokens, 32 query and 8 KV heads of 128 (604 MB): 137 us = 4.4 TB/s, 0.65 of the copy
-// rate (the same walk without arithmetic: 98 us); one such sequence 23.4 us.  On the way, for
-// the 16: one warp per key in fp32 4612 us; tensor cores on converted registers 199; q and the
-// weights as the A operand 197; codes as the A operand with the heads twice 132, centred 155,
-// one LOP3 per pair 147, K as subnormals 137.  12 warps of 168 registers: 218 us at the 132 step.
+// Bound by instructions: about 790 per warp and block of 32 keys, 0.57 issued per cycle and
+// scheduler by 4 warps of 128 registers.  16 sequences of 32768 tokens, 32 query and 8 KV heads
+// of 128 (604 MB): 138 us = 4.4 TB/s, 0.64 of the copy rate (the same walk without arithmetic: 98
+// us); one such sequence 22.2 us.  On the way, for the 16: one warp per key in fp32 4612 us;
+// tensor cores on converted registers 199; q and the weights as the A operand 197; codes as the
+// A operand with the heads twice 132, centred 155, one LOP3 per pair 147, K as subnormals 138.
+// 12 warps of 168 registers: 218 us at the 132 step.
 #include <cuda_fp16.h>
 
 #include "santa_split.cuh"
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
             if (fresh) {
                 fresh = false;
                 // q as the B operand: word u's step s takes elements (2s, 2s + 4) and (2s + 1, 2s + 5) of
-                // words kW t + u of the head of column g, the latter / 16 because their codes are high nibbles
+                // words kW t + u of the head of column g
                 const int hg = kTwice ? g & 3 : g;
                 const Q *qh = static_cast<const Q *>(p.q) +
                               (size_t(w.heads[sel].b) * p.Hq + w.heads[sel].kvh * G + min(hg, G - 1)) * D + t * kW * 8;
@@ -348,25 +347,25 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     for (int i = 0; i < kG; ++i) sum[i] += __shfl_xor_sync(kFull, sum[i], s);
                 }
                 const int e = exponent(mx);
-                const float f = pow2(14 - e), fh = f * 0.0625f;
+                const float f = pow2(14 - e);
 #pragma unroll
                 for (int u = 0; u < kW; ++u) {
                     float a[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * (i & 1 ? fh : f);
+                    for (int i = 0; i < 8; ++i) a[i] = x[u][i] * f;
 #pragma unroll
                     for (int part = 0; part < kQ; ++part)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) qf[part][u][i] = half_pair(a[i], a[i + 4]);
                 }
-                // y = sum_g s_g c_g + m_g sum(q_g) / (2^24 2^(e - 14)), in the products' units
+                // y = sum_g s_g c_g + m_g sum(q_g) / (2^20 2^(e - 14)), in the products' units
                 const int e0 = __shfl_sync(kFull, e, 4 * h0), e1 = __shfl_sync(kFull, e, 4 * (h0 + 1));
                 const float scale2 = p.scale * 1.4426950408889634f;
-                kq = make_float2(pow2(e0 + 10) * scale2, pow2(e1 + 10) * scale2);
+                kq = make_float2(pow2(e0 + 6) * scale2, pow2(e1 + 6) * scale2);
 #pragma unroll
                 for (int i = 0; i < kG; ++i)
-                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(-10 - e0),
-                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(-10 - e1));
+                    qsum[i] = make_float2(__shfl_sync(kFull, sum[i], 4 * h0) * pow2(-6 - e0),
+                                          __shfl_sync(kFull, sum[i], 4 * (h0 + 1)) * pow2(-6 - e1));
             }
             if constexpr (kTma) {
                 if (!mbar_wait(&bars[cur], phase >> cur & 1)) {
@@ -423,14 +422,17 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                 for (int u = 0; u < kW; ++u)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint32_t a = kc[2 * mt][u] >> (8 * s), b = kc[2 * mt + 1][u] >> (8 * s);
+                        // nibbles 2s (and 2s + 4), then 2s + 1 (and 2s + 5), each at bits 4 .. 7
+                        const uint32_t ka = kc[2 * mt][u], kb = kc[2 * mt + 1][u];
+                        const uint32_t a0 = (s ? ka >> 4 : ka << 4) & kHigh, a1 = (s ? ka >> 8 : ka) & kHigh;
+                        const uint32_t b0 = (s ? kb >> 4 : kb << 4) & kHigh, b1 = (s ? kb >> 8 : kb) & kHigh;
 #pragma unroll
                         for (int part = kQ - 1; part >= 0; --part) {
                             if (u < kG && s == 0 && part == kQ - 1)
-                                mma_f16_zero(c[u % kG], a & kLow, b & kLow, a & kHigh, b & kHigh, qf[part][u][2 * s],
+                                mma_f16_zero(c[u % kG], a0, b0, a1, b1, qf[part][u][2 * s],
                                              qf[part][u][2 * s + 1]);
                             else
-                                mma_f16(c[u % kG], a & kLow, b & kLow, a & kHigh, b & kHigh, qf[part][u][2 * s],
+                                mma_f16(c[u % kG], a0, b0, a1, b1, qf[part][u][2 * s],
                                         qf[part][u][2 * s + 1]);
                         }
                     }
