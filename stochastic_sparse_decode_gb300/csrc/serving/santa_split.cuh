@@ -490,9 +490,9 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
             // the CTA's part is visible (the barrier above, this fence) before it is counted
             __threadfence();
             unsigned *cnt = sp.cnt + size_t(sh.inc_b[k]) * p.Hkv + sh.inc_kvh[k];
-            if (atomicAdd(cnt, 1u) == unsigned(sh.inc_parts[k] - 1)) {
+            const unsigned end = unsigned(sh.inc_parts[k] - 1);
+            if (atomicInc(cnt, end) == end) {  // which sets it back to 0
                 sh.last[k] = 1;
-                *cnt = 0u;
                 __threadfence();  // the others' parts are read after their counts
             }
         }

@@ -641,6 +641,25 @@ def test_kv4_append_and_read(dtype, d, T, hkv, fused):
     assert (cache[rest] == 0xAB).all()
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_kv4_ties_between_codes(dtype, d):
+    """Values in the middle between two codes, and a unit in the last place beside it: as the division rounds."""
+    dt = DT[dtype]
+    step = 2.0 ** torch.arange(-6, 6, device="cuda").double()[:, None, None]
+    half = torch.arange(d, device="cuda").double() % 31 / 2  # 0, 0.5, .. 15: every group has 0 and 15
+    k = (half * step).to(dt).expand(12, 1, d).contiguous()
+    v = k.clone()
+    near = torch.nextafter(k.float(), torch.full_like(k, 1e9, dtype=torch.float32)) if dt == torch.float32 else k.float()
+    v[:] = torch.where((half % 1 == 0.5).expand_as(k), near.to(dt), k)
+    dec = Decoder(1, 1, 1, d, 12, 12, 256, 1, dtype)
+    cache = dec.kv4_cache()
+    dec.kv4_append(k, v, None, cache)
+    for x, a, b in ((k, 0, d), (v, d // 2, d + d // 16)):
+        codes, pairs = _quantised(x)
+        assert np.array_equal(cache[..., a:a + d // 2].cpu().numpy(), codes)
+        assert np.array_equal(cache[..., b:b + d // 16].contiguous().view(torch.float16).cpu().numpy().reshape(pairs.shape), pairs)
+
+
 def test_kv4_special_values_and_slots():
     T, d = 6, 64
     k = torch.randn((T, 1, d), device="cuda")
