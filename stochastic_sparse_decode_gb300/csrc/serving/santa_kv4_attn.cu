@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                     fscale = f;
                 }
                 if (!kTma && more) load_par(next, next_seen);
-                // per key and group (s, s, m, m) of K, then (s, s, m + 8 s, twice) of V; the slots of a key turn with the key
-                // against bank conflicts
+                // per key and group (s, s, m, m) of K, then (s, s, m + 8 s, m + 8 s) of V; the slots of a
+                // key turn with the key against bank conflicts
 #pragma unroll
                 for (int i = 0; i < 2 * kG; ++i) {
                     const float sc = i < kG ? sm[i].x : sm[i].x * fscale;
@@ -532,9 +532,11 @@ __global__ void __launch_bounds__(Kv4Geom<D, Q, GT>::kWarps * 32, 1)
                                 const uint32_t(&b)[4] = pf[i % kG][part];
                                 const uint32_t a = pr[2 * ks], c = pr[2 * ks + 1];
                                 if (ks == 0 && part == kParts - 1)
-                                    mma_f16_zero(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks], b[2 * ks + 1]);
+                                    mma_f16_zero(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks],
+                                                 b[2 * ks + 1]);
                                 else
-                                    mma_f16(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks], b[2 * ks + 1]);
+                                    mma_f16(acc, low_codes(a), high_codes(a), low_codes(c), high_codes(c), b[2 * ks],
+                                            b[2 * ks + 1]);
                             }
                         float(&o)[4] = O[4 * i + 2 * half + s];
                         const float2 lo = __ffma2_rn(make_float2(o[0], o[1]), sco, make_float2(acc[0], acc[1]));

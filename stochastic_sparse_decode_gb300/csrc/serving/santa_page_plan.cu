@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     pdl_launch_dependents();
     long long tok0 = 0, page0 = 0;  // of the tiles before
     if (tid < 2) s_sum[tid] = 0;
+    __syncthreads();
     for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int len = 0, nw = 0;

@@ -8,8 +8,8 @@
 // one per warp of the grid, so that every warp has the same number of units, to one,
 // whatever the lengths are; lengths are read on the device, and each warp works out its
 // own stretch.  (Where that costs more than it gives, kJoinUnits, each CTA takes one head
-// instead, and nothing is joined across CTAs.)  A warp keeps an online softmax (M, Z, O) per query head and closes it
-// when its stretch leaves a head:
+// instead, and nothing is joined across CTAs.)  A warp keeps an online softmax (M, Z, O) per
+// query head and closes it when its stretch leaves a head:
 //   - a head that lies within the stretch is finished by the warp itself;
 //   - a head shared by warps of one CTA only is joined through shared memory;
 //   - a head shared by CTAs: each CTA joins its warps' pieces, stores one part in the
