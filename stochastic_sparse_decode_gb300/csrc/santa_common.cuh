@@ -236,6 +236,14 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A plain load, for the inputs of a kernel that is launched so.  Such a kernel may start while
+// the one before it still writes what it reads, and the read-only path (__ldg) is defined only
+// for memory that stays as it is while the kernel lives: its loads may move ahead of the wait.
+template <typename T>
+__device__ __forceinline__ T load(const T *p) {
+    return *p;
+}
+
 // ------------------------------------------------------------------ element types
 
 // K/V/q storage: bf16 is carried as its 16-bit pattern.
@@ -425,7 +433,7 @@ __device__ __forceinline__ int seq_bounds(const Params &p, int b, long long *sta
 template <bool kPaged>
 __device__ __forceinline__ long long key_row(const Params &p, int b, long long start, int i) {
     if constexpr (!kPaged) return start + i;
-    const int pg = __ldg(p.page_table + (size_t)b * p.max_pages + i / p.page_size);
+    const int pg = load(p.page_table + (size_t)b * p.max_pages + i / p.page_size);
     if (pg < 0 || pg >= p.num_pages) {
         raise_flag(p, SANTA_ERR_INDPTR);
         return -1;

@@ -217,13 +217,13 @@ __device__ __forceinline__ void gather_queue(float (&acc)[D / 32], const T *vrow
                 const unsigned char *src = reinterpret_cast<const unsigned char *>(vrow0 + size_t(jr) * row_stride) +
                                            lane * kBytes;
                 if constexpr (kWords == 1) {
-                    raw[r][0] = __ldg(reinterpret_cast<const unsigned int *>(src));
+                    raw[r][0] = load(reinterpret_cast<const unsigned int *>(src));
                 } else if constexpr (kWords == 2) {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src));
+                    const uint2 w = load(reinterpret_cast<const uint2 *>(src));
                     raw[r][0] = w.x;
                     raw[r][1] = w.y;
                 } else {
-                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src));
+                    const uint4 w = load(reinterpret_cast<const uint4 *>(src));
                     raw[r][0] = w.x;
                     raw[r][1] = w.y;
                     raw[r][2] = w.z;
@@ -330,7 +330,7 @@ __device__ void sample_head(const Params &p, int b, int hq, int split, unsigned 
         for (int i = tid; i < nu; i += kSampThreads) {
             float x = INFINITY;  // padding sorts last
             if (i < p.S) {
-                x = __ldg(ug + i);
+                x = load(ug + i);
                 if (!(x >= 0.f && x < 1.f)) {
                     raise_flag(p, SANTA_ERR_OFFSET);
                     x = x >= 1.f ? nextafterf(1.f, 0.f) : 0.f;
@@ -644,7 +644,7 @@ __device__ void sample_head(const Params &p, int b, int hq, int split, unsigned 
                 if constexpr (kPaged) {
                     if (lane < ne) {
                         const int ck = l_c[ea + lane];
-                        int pg = __ldg(p.page_table + size_t(b) * p.max_pages + (ck * kChunkRows) / p.page_size);
+                        int pg = load(p.page_table + size_t(b) * p.max_pages + (ck * kChunkRows) / p.page_size);
                         if (pg < 0 || pg >= p.num_pages) {  // bad page id: flagged, row 0 read instead
                             raise_flag(p, SANTA_ERR_INDPTR);
                             pg = -1;

@@ -124,7 +124,7 @@ __device__ __forceinline__ void load_q_slice(const Params &p, int b, int hq0, in
     for (int h = 0; h < GH; ++h)
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(qh + (h ^ hx) * D + (l8 + 8 * i) * Geo::kEV));
+            const uint4 raw = load(reinterpret_cast<const uint4 *>(qh + (h ^ hx) * D + (l8 + 8 * i) * Geo::kEV));
             Vec16<T>::unpack(raw, &qreg[h][i * PAIRS]);
         }
 }
@@ -146,8 +146,8 @@ __device__ __forceinline__ void load_q_frag(const Params &p, int b, int hq0, int
                                                             (size_t(b) * p.Hq + hq0 + min(g, G - 1)) * D);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][0] = g < G ? __ldg(qh + 8 * ks + t) : 0u;
-        qf[ks][1] = g < G ? __ldg(qh + 8 * ks + 4 + t) : 0u;
+        qf[ks][0] = g < G ? load(qh + 8 * ks + t) : 0u;
+        qf[ks][1] = g < G ? load(qh + 8 * ks + 4 + t) : 0u;
     }
 }
 

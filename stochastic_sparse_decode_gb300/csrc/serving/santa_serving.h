@@ -8,16 +8,6 @@ namespace santa {
 
 constexpr int kMaxGroup = 8;  // query heads of one KV head, at most
 
-#ifdef __CUDACC__
-// A plain load.  These kernels start while the kernel before them in the stream still writes
-// what they read (programmatic dependent launch), so nothing may go by the read-only path,
-// whose loads the compiler is free to move ahead of the wait.
-template <typename T>
-__device__ __forceinline__ T load(const T *p) {
-    return *p;
-}
-#endif
-
 struct PlanParams {
     int batch, page_size, max_pages, num_free, max_tokens;
     long long num_pages;

@@ -937,3 +937,83 @@ def test_rows_beyond_32_bit_offsets():
         for got, (kk, vv) in ((out, (k4, v4)), (win, (k[:, h].double(), v[:, h].double()))):
             want, tol = _attention_reference(q[:1, h].double(), kk, vv, 1 / math.sqrt(d), 2.0 ** -22)
             assert ((got[0, h].double() - want[0]).abs() <= tol[0]).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_plan_and_rotation_in_front_of_the_sampled_decodes(dtype, d):
+    """santa_page_plan and santa_norm_rope let their successor start before they have written the page table, the
+    queries and the caches that it reads.  Steps queued one behind another, and steps replayed from a graph, equal
+    bit for bit the steps with a synchronisation between the calls (paged prop, and the fused and two-kernel prop
+    on contiguous rows)."""
+    B, hq, hkv, page, max_pages, S, steps = 6, 8, 2, 32, 40, 32, 12
+    num_pages, dt = B * max_pages, DT[dtype]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(60)
+    rows = num_pages * page
+    dec = Decoder(B, hq, hkv, d, rows, max_pages * page, 256, S, dtype)
+    modes = ("paged", "prop", "prop_fused")
+    for m in ("prop", "prop_fused"):
+        dec.workspace(m)
+    cs = rope_table(max_pages * page, d)
+    w = (1 + 0.3 * torch.randn(d, generator=gen, device="cuda")).to(dt)
+    lens0 = torch.randint(20, (max_pages - 1) * page, (B,), generator=gen, **i32)
+    table0 = torch.randperm(num_pages, generator=gen, device="cuda").to(torch.int32).reshape(B, max_pages)
+    have = (lens0 + page - 1) // page
+    free0 = torch.cat([table0[b, int(have[b]):] for b in range(B)])
+    for b in range(B):
+        table0[b, int(have[b]):] = -5  # what the plan enters is read, not what lay there
+    pools0 = [torch.randn((rows, hkv, d), generator=gen, device="cuda").to(dt) for _ in range(2)]
+    qkvs = torch.randn((steps, B, hq + 2 * hkv, d), generator=gen, device="cuda").to(dt)
+    U = torch.rand((B, hq), generator=gen, device="cuda") / S * 0.999
+    indptr = torch.arange(B + 1, device="cuda") * (max_pages * page)
+    new = torch.ones(B, **i32)
+    s = dict(lens=lens0.clone(), table=table0.clone(), free=free0.clone(), k=pools0[0].clone(), v=pools0[1].clone(),
+             qkv=qkvs[0].clone(), slots=torch.empty(B, dtype=torch.int64, device="cuda"), pos=torch.empty(B, **i32),
+             lens_out=torch.empty(B, **i32), counts=torch.empty(2, **i32))
+    outs = {m: torch.empty((B, hq, d), device="cuda") for m in modes}
+    qr = torch.empty((B, hq, d), dtype=dt, device="cuda")
+
+    def restart():
+        for name, t in (("lens", lens0), ("table", table0), ("free", free0), ("k", pools0[0]), ("v", pools0[1])):
+            s[name].copy_(t)
+
+    def step(pause):
+        x = s["qkv"]
+        dec.page_plan(s["lens"], new, s["table"], s["free"], page, s["slots"], s["pos"], s["lens_out"], s["counts"])
+        pause()
+        dec.norm_rope(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], s["pos"], s["slots"], cs, s["k"], s["v"], w, w, out=qr)
+        pause()
+        dec.prop_paged(qr, s["k"], s["v"], s["table"], s["lens_out"], page, U, out=outs["paged"])
+        pause()
+        dec.norm_rope(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], s["pos"], s["slots"], cs, s["k"], s["v"], out=qr)
+        pause()
+        dec("prop", qr, s["k"], s["v"], indptr, U, out=outs["prop"])
+        pause()
+        dec.norm_rope(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], s["pos"], s["slots"], cs, s["k"], s["v"], w, None, out=qr)
+        pause()
+        dec("prop_fused", qr, s["k"], s["v"], indptr, U, out=outs["prop_fused"])
+        pause()
+
+    def run(one):
+        restart()
+        got = []
+        for i in range(steps):
+            s["qkv"].copy_(qkvs[i])
+            one()
+            got.append([outs[m].clone() for m in modes] + [qr.clone(), s["slots"].clone(), s["lens_out"].clone()])
+            s["free"].copy_(torch.roll(s["free"], -int(s["counts"][0])))  # taken pages go to the end
+            s["lens"].copy_(s["lens_out"])
+        torch.cuda.synchronize()
+        return got
+
+    want = run(lambda: step(torch.cuda.synchronize))
+    for a in want:
+        assert all(torch.isfinite(x.float()).all() for x in a[:4]) and (a[4] >= 0).all()
+    eager = run(lambda: step(lambda: None))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(lambda: None)
+    replayed = run(graph.replay)
+    for a, b, c in zip(want, eager, replayed):
+        for x, y, z in zip(a, b, c):
+            assert torch.equal(x, y) and torch.equal(x, z)

@@ -1,6 +1,8 @@
 """Refusals of the operators around the attention, on the host: no call here reaches a kernel launch."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -165,3 +167,20 @@ def test_decoder_refuses_tensors_the_call_would_misread(sd):
         dec.kv4_append(k[:4], k[:4], torch.zeros(4, dtype=torch.int32), torch.zeros(1))
     with pytest.raises(ValueError):
         dec.page_plan(ind.int(), ind.int(), ind.int()[None], ind.int(), 33, ind, ind.int(), ind.int(), ind.int()[:2])
+
+
+def test_kernels_launched_early_read_nothing_by_the_read_only_path():
+    """A kernel launched with programmatic dependent launch may start while page plan, norm + rotation or the 4-bit
+    read (which let their successor start at once) still write its page table, queries or caches; the read-only
+    path is for memory that no one writes while the kernel lives.  The files of such kernels: the streaming pass
+    and the fused sampler of prop, and the serving operators."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "stochastic_sparse_decode_gb300",
+                        "csrc")
+    files = [os.path.join(csrc, f) for f in ("santa_stream.cuh", "santa_sampler.cuh")]
+    files += [os.path.join(csrc, "serving", f) for f in sorted(os.listdir(os.path.join(csrc, "serving")))]
+    bad = re.compile(r"__ldg\s*\(|ld\.global\.nc|ld\.global\.\w+\.nc|__restrict__")
+    for f in files:
+        assert not bad.search(re.sub(r"//[^\n]*", "", open(f).read())), f
+    common = open(os.path.join(csrc, "santa_common.cuh")).read()
+    body = re.search(r"long long key_row\(.*?\n}\n", common, re.S).group(0)  # pass 1's page lookup
+    assert not bad.search(body)
