@@ -487,7 +487,10 @@ typedef struct {
  *              one (padding) leaves the cache as it is; NULL: token t is row t.
  *              Rows must be distinct: of two tokens with one row either's elements stay
  *   q_out      [num_tokens][Hq][d]; q itself may be given if its rows are contiguous
- *   k_cache, v_cache  [total_tokens][Hkv][d], the cache (or the page pools)
+ *   k_cache, v_cache  [total_tokens][Hkv][d], the cache (or the page pools).  Without
+ *              a slot map rows 0 .. num_tokens - 1 alone are written, so a buffer of
+ *              num_tokens <= total_tokens rows will do: the rotated keys as
+ *              santa_kv4_append takes them
  * q with q_out, k with k_cache and v with v_cache may each be NULL (left out); v is
  * copied.  Queries of padding tokens are computed like the others.
  */

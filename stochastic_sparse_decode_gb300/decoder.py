@@ -280,6 +280,15 @@ class Decoder:
                 return t.data_ptr(), s[0] if n > 1 else heads * d
         self._refuse(name, t, self._dt, (n, heads, d), dev, "row by row ")
 
+    def _token_rows(self, name, t, slot_map, n, dev):
+        """Refuses what is not a buffer of a row per token in the place of a cache."""
+        rows = self.problem.total_tokens
+        if slot_map is not None or n > rows:  # the call writes no row beyond the cache's
+            self._refuse(name, t, self._dt, self._kv_shape, dev)
+        shape = (n, *self._kv_shape[1:])
+        if not _fits(t, self._dt, shape, dev):
+            self._refuse(name, t, self._dt, shape, dev)
+
     def kv4_append(self, k, v, slot_map, kv4, debug=None, stream=None) -> torch.Tensor:
         """Stores tokens k, v [tokens][Hkv][d] into rows slot_map of the 4-bit cache (santa_kv4_append)."""
         h, n, dev = self.problem.num_kv_heads, k.shape[0], k.get_device()
@@ -316,7 +325,9 @@ class Decoder:
                   eps=1e-6, interleaved=False, out=None, debug=None, stream=None):
         """Norms and rotation of the step's q [tokens][Hq][d] and k [tokens][Hkv][d]; k and v go to rows slot_map
         of the caches (santa_norm_rope).  cos_sin: rope_table.  Returns the rotated queries.  q, or k with
-        k_cache, or v with v_cache may be None."""
+        k_cache, or v with v_cache may be None.  Without a slot map token t goes to row t, and k_cache and v_cache
+        may also be [tokens][Hkv][d], with at most total_tokens tokens: the rotated keys by themselves, as
+        kv4_append takes them."""
         p, dev = self.problem, positions.get_device()
         n, d = positions.shape[0], p.head_dim
         if not _fits(positions, _I32, (n,), dev):
@@ -339,11 +350,11 @@ class Decoder:
             vp, vs = self._rows("v", v, n, p.num_kv_heads, dev)
         if k_cache is not None:
             if not _fits(k_cache, self._dt, self._kv_shape, dev):
-                self._refuse("k_cache", k_cache, self._dt, self._kv_shape, dev)
+                self._token_rows("k_cache", k_cache, slot_map, n, dev)
             kc = k_cache.data_ptr()
         if v_cache is not None:
             if not _fits(v_cache, self._dt, self._kv_shape, dev):
-                self._refuse("v_cache", v_cache, self._dt, self._kv_shape, dev)
+                self._token_rows("v_cache", v_cache, slot_map, n, dev)
             vc = v_cache.data_ptr()
         if q_weight is not None:
             if not _fits(q_weight, self._dt, (d,), dev):

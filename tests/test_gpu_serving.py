@@ -1017,3 +1017,93 @@ def test_plan_and_rotation_in_front_of_the_sampled_decodes(dtype, d):
     for a, b, c in zip(want, eager, replayed):
         for x, y, z in zip(a, b, c):
             assert torch.equal(x, y) and torch.equal(x, z)
+
+
+# ------------------------------------------------------------------------------ README's steps, keys from their tokens
+
+
+def _readme_step(call):
+    """README's code block that makes `call`, comments apart."""
+    import os
+    import re
+
+    readme = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    blocks = [re.sub(r"#[^\n]*", "", b) for b in re.findall(r"```python\n(.*?)```", open(readme).read(), re.S)]
+    found = [b for b in blocks if f"dec.{call}(" in b]
+    assert len(found) == 1, (call, len(found))
+    return found[0]
+
+
+@pytest.mark.parametrize("call", ["window_paged", "kv4_paged"])
+def test_readme_step_as_written(call):
+    """The step that README shows, run as it stands on a cache that earlier steps filled: the new token's row of the
+    cache holds its key normalised and rotated to its position (worked out here from the raw key in 64 bits), its
+    value, and the output is the attention over those."""
+    B, hq, hkv, d, page_size, max_pages = 3, 8, 2, 128, 32, 5
+    gen = torch.Generator(device="cuda").manual_seed(70)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rows = B * max_pages * page_size
+    dec = Decoder(B, hq, hkv, d, rows, max_pages * page_size, 256, 1, "bf16")
+    lens = [70, 31, 96]
+    q0, k0, v0 = rnd(B, hq, d), rnd(B, hkv, d), rnd(B, hkv, d)
+    qw, kw = (1 + 0.3 * rnd(d).float()).bfloat16(), (1 + 0.3 * rnd(d).float()).bfloat16()
+    table = torch.arange(B * max_pages, **i32).reshape(B, max_pages).flip(0).contiguous()
+    k_pool, v_pool, kv4 = rnd(rows, hkv, d), rnd(rows, hkv, d), dec.kv4_cache()
+    dec.kv4_append(k_pool, v_pool, None, kv4)
+    names = dict(dec=dec, torch=torch, q=q0.clone(), k=k0.clone(), v=v0.clone(), kv_lens=torch.tensor(lens, **i32),
+                 new_lens=torch.ones(B, **i32), page_table=table, free_pages=torch.tensor([6, 7, 8, 9], **i32),
+                 page_size=page_size, slot_map=torch.empty(B, dtype=torch.int64, device="cuda"),
+                 positions=torch.empty(B, **i32), lens_out=torch.empty(B, **i32), counts=torch.empty(2, **i32),
+                 cos_sin=rope_table(200, d), k_pool=k_pool, v_pool=v_pool, kv4=kv4, q_weight=qw, k_weight=kw)
+    exec(_readme_step(call), names)
+    assert names["lens_out"].tolist() == [n + 1 for n in lens]
+    cs = names["cos_sin"][torch.tensor(lens, device="cuda")]
+    kr, kmag = _rope_reference(k0, kw, 1e-6, cs, d, False)
+    qr, qmag = _rope_reference(q0, qw, 1e-6, cs, d, False)
+    _close(names["q"], qr, qmag, "q")
+    for b, n in enumerate(lens):
+        i = np.arange(n + 1)
+        where = torch.from_numpy(names["page_table"].cpu().numpy()[b, i // page_size].astype(np.int64) * page_size + i % page_size).cuda()
+        for h in range(hkv):
+            if call == "kv4_paged":
+                k, v = _values64(kv4[where, h], d)
+                x, y = kr[b, h].bfloat16().double(), v0[b, h].double()
+                # a code is off by half a step of the group's scale at most, and the scale (15 of them) and the minimum by
+                # a rounding to fp16 (2^-11); the key, and the extremes of its group, by a step of bf16 (2^-7) before
+                for got, want in ((k[-1], x), (v[-1], y)):
+                    g = (torch.arange(d, device="cuda") // 8) % (d // 64)
+                    lo, hi = (torch.stack([f(want[g == j]) for j in range(d // 64)])[g] for f in (torch.min, torch.max))
+                    tol = (hi - lo) / 15 * (0.5 + 2.0 ** -6) + (2.0 ** -7 + 2.0 ** -10) * torch.maximum(lo.abs(), hi.abs())
+                    assert ((got - want).abs() <= tol).all(), (b, h)
+                keep = slice(None)
+            else:
+                k, v = k_pool[where, h].double(), v_pool[where, h].double()
+                _close(k_pool[where[-1:], h], kr[b, h][None], kmag[b, h][None], "k")
+                assert torch.equal(v[-1], v0[b, h].double())
+                keep = torch.tensor(_seen(n + 1, 4096, 4), device="cuda")
+            heads = slice(4 * h, 4 * h + 4)
+            want, tol = _attention_reference(names["q"][b, heads].double(), k[keep], v[keep], 1 / math.sqrt(d), 2.0 ** -22)
+            assert ((names["out"][b, heads].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_norm_rope_into_a_row_per_token(dtype, d):
+    """Without a slot map a buffer of a row per token takes the rotated keys and the values: as rows of a whole cache."""
+    dt, T, hkv = DT[dtype], 21, 3
+    k, v = (torch.randn((T, hkv, d), device="cuda").to(dt) for _ in range(2))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 5
+    dec, cs = Decoder(1, hkv, hkv, d, 50, 50, 256, 1, dtype), rope_table(64, d)
+    kc, vc = (torch.zeros((50, hkv, d), dtype=dt, device="cuda") for _ in range(2))
+    kt, vt = torch.zeros_like(k), torch.zeros_like(v)
+    dec.norm_rope(None, k, v, pos, None, cs, kc, vc)
+    dec.norm_rope(None, k, v, pos, None, cs, kt, vt)
+    assert torch.equal(kt, kc[:T]) and torch.equal(vt, v) and not kc[T:].any()
+    slots = torch.arange(T, device="cuda")
+    for bad in (dict(k_cache=kt, v_cache=vc, slot_map=slots), dict(k_cache=kc, v_cache=vt, slot_map=slots),
+                dict(k_cache=kt[:-1], v_cache=vt, slot_map=None)):
+        with pytest.raises(ValueError, match="_cache: shape"):
+            dec.norm_rope(None, k, v, pos, bad["slot_map"], cs, bad["k_cache"], bad["v_cache"])
+    few = Decoder(1, hkv, hkv, d, T - 1, T - 1, 256, 1, dtype)  # fewer rows than tokens: rows would be dropped
+    with pytest.raises(ValueError, match="k_cache: shape"):
+        few.norm_rope(None, k, v, pos, None, cs, kt, vt)
