@@ -187,8 +187,9 @@ int santa_norm_rope(const santa_problem *p, const santa_rope *r, int num_tokens,
     if (!r || num_tokens < 0 || num_tokens > kMaxRows) return SANTA_INVALID_ARG;
     if (r->rot_dim <= 0 || r->rot_dim > p->head_dim || r->max_pos < 1 || !(r->eps >= 0.f)) return SANTA_INVALID_ARG;
     if (r->rot_dim % 16 != 0) return SANTA_UNSUPPORTED;
+    if (num_tokens == 0) return SANTA_OK;  // before the pairs: an empty tensor has no address, its cache has one
     if (!q != !q_out || !k != !k_cache || !v != !v_cache) return SANTA_INVALID_ARG;
-    if (num_tokens == 0 || (!q && !k && !v)) return SANTA_OK;
+    if (!q && !k && !v) return SANTA_OK;
     if (!r->cos_sin || !positions || !aligned(r->cos_sin, 16) || !aligned(positions, 4) || !aligned(slot_map, 8) ||
         !aligned(r->q_weight, 16) || !aligned(r->k_weight, 16))
         return SANTA_INVALID_ARG;

@@ -1107,3 +1107,20 @@ def test_norm_rope_into_a_row_per_token(dtype, d):
     few = Decoder(1, hkv, hkv, d, T - 1, T - 1, 256, 1, dtype)  # fewer rows than tokens: rows would be dropped
     with pytest.raises(ValueError, match="k_cache: shape"):
         few.norm_rope(None, k, v, pos, None, cs, kt, vt)
+
+
+def test_a_step_without_a_token():
+    """No new token at all: rotation, store and read back take empty tensors and leave the caches as they are."""
+    hq, hkv, d, rows = 4, 2, 64, 32
+    dec = Decoder(1, hq, hkv, d, rows, rows, 256, 1, "bf16")
+    qkv = torch.empty((0, hq + 2 * hkv, d), dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    kc, vc = (torch.ones((rows, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kv4 = dec.kv4_cache()
+    pos, slots = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    cs = rope_table(rows, d)
+    assert dec.norm_rope(q, k, v, pos, slots, cs, kc, vc).shape == (0, hq, d)
+    assert dec.norm_rope(q, k, v, pos, None, cs, torch.empty_like(k), torch.empty_like(v)).shape == (0, hq, d)
+    dec.kv4_append(k, v, slots, kv4)
+    assert [tuple(x.shape) for x in dec.kv4_read(kv4, slots)] == [(0, hkv, d)] * 2
+    assert (kc == 1).all() and (vc == 1).all() and not kv4.any()

@@ -184,3 +184,10 @@ def test_kernels_launched_early_read_nothing_by_the_read_only_path():
     common = open(os.path.join(csrc, "santa_common.cuh")).read()
     body = re.search(r"long long key_row\(.*?\n}\n", common, re.S).group(0)  # pass 1's page lookup
     assert not bad.search(body)
+
+
+def test_norm_rope_of_no_token(sd):
+    """A step without a token: empty tensors have no address, the caches do."""
+    assert _rope(sd, n=0, q=None, k=None, v=None) == sd.OK
+    assert _rope(sd, n=0, q=None, q_out=None, k=None, v=None, positions=None, slot_map=None) == sd.OK
+    assert _rope(sd, n=0, r=dict(rot_dim=0)) == sd.INVALID_ARG
