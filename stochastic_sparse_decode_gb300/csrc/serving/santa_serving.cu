@@ -61,8 +61,9 @@ SplitLayout split_layout(const santa_problem *p) {
     return L;
 }
 
-int attend(const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q, const void *k,
-           const void *v, const void *kv4, const long long *kv_indptr, float *out, void *workspace,
+// The attention over a cache of k and v, or, with `four_bit`, over kv4.
+int attend(bool four_bit, const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
+           const void *k, const void *v, const void *kv4, const long long *kv_indptr, float *out, void *workspace,
            size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream_) {
     int st = check_split(p);
     if (st != SANTA_OK) return st;
@@ -82,10 +83,9 @@ int attend(const santa_problem *p, const santa_window *w, const santa_pages *pag
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || (kv_indptr && !aligned(kv_indptr, 8)))
         return SANTA_INVALID_ARG;
     const bool empty = p->max_len == 0 || p->total_tokens == 0;  // no sequence can hold a key
-    const bool no_cache = !kv4 && (!k || !v);
-    if (!kv4 && (k || v) && (no_cache || !aligned(k, 16) || !aligned(v, 16))) return SANTA_INVALID_ARG;
-    if (kv4 && !aligned(kv4, 16)) return SANTA_INVALID_ARG;
-    if (no_cache && !empty) return SANTA_INVALID_ARG;
+    const bool no_cache = four_bit ? !kv4 : !k || !v;
+    if (no_cache && (!empty || k || v)) return SANTA_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv4, 16)) return SANTA_INVALID_ARG;
     const SplitLayout L = split_layout(p);
     if (workspace_bytes < L.total) return SANTA_WORKSPACE_TOO_SMALL;
 
@@ -129,7 +129,7 @@ int attend(const santa_problem *p, const santa_window *w, const santa_pages *pag
         tm.begin = reinterpret_cast<cudaEvent_t>(dbg->main_begin);
         tm.end = reinterpret_cast<cudaEvent_t>(dbg->main_end);
     }
-    return status(kv4 ? launch_kv4(sp, p->dtype, stream, tm) : launch_window(sp, p->dtype, stream, tm));
+    return status(four_bit ? launch_kv4(sp, p->dtype, stream, tm) : launch_window(sp, p->dtype, stream, tm));
 }
 
 }  // namespace
@@ -302,14 +302,13 @@ int santa_decode_window(const santa_problem *p, const santa_window *w, const san
                         const void *k, const void *v, const long long *kv_indptr, float *out, void *workspace,
                         size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream) {
     if (!w) return SANTA_INVALID_ARG;
-    return attend(p, w, pages, q, k, v, nullptr, kv_indptr, out, workspace, workspace_bytes, dbg, stream);
+    return attend(false, p, w, pages, q, k, v, nullptr, kv_indptr, out, workspace, workspace_bytes, dbg, stream);
 }
 
 int santa_decode_kv4(const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
                      const void *kv4, const long long *kv_indptr, float *out, void *workspace,
                      size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream) {
-    if (!kv4) return SANTA_INVALID_ARG;
-    return attend(p, w, pages, q, nullptr, nullptr, kv4, kv_indptr, out, workspace, workspace_bytes, dbg, stream);
+    return attend(true, p, w, pages, q, nullptr, nullptr, kv4, kv_indptr, out, workspace, workspace_bytes, dbg, stream);
 }
 
 }  // extern "C"

@@ -1124,3 +1124,17 @@ def test_a_step_without_a_token():
     dec.kv4_append(k, v, slots, kv4)
     assert [tuple(x.shape) for x in dec.kv4_read(kv4, slots)] == [(0, hkv, d)] * 2
     assert (kc == 1).all() and (vc == 1).all() and not kv4.any()
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+@pytest.mark.parametrize("rows,max_len,page", [(0, 64, 0), (64, 0, 0), (0, 0, 0), (64, 0, 32)])
+def test_attention_without_a_key_gives_zeros(kind, rows, max_len, page):
+    """A cache of no row, or sequences that may hold no key."""
+    dec = Decoder(2, 4, 2, 64, rows, max_len, 256, 1, "bf16")
+    q = torch.randn((2, 4, 64), device="cuda").bfloat16()
+    pools = [torch.empty((rows, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    addr = dict(indptr=torch.zeros(3, dtype=torch.int64, device="cuda"),
+                table=torch.zeros((2, 2), dtype=torch.int32, device="cuda"), lens=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    out = torch.full((2, 4, 64), 7.0, device="cuda")
+    _run_attention(kind, dec, q, [dec.kv4_cache()] if kind == "kv4" else pools, addr, page, 10, 2, out=out)
+    assert not out.any()

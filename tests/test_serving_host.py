@@ -191,3 +191,15 @@ def test_norm_rope_of_no_token(sd):
     assert _rope(sd, n=0, q=None, k=None, v=None) == sd.OK
     assert _rope(sd, n=0, q=None, q_out=None, k=None, v=None, positions=None, slot_map=None) == sd.OK
     assert _rope(sd, n=0, r=dict(rot_dim=0)) == sd.INVALID_ARG
+
+
+def test_kv4_of_nothing_needs_no_cache(sd):
+    """As the windowed call: no sequence, or no key, and the cache's address is not asked for (an empty tensor has
+    none).  With keys it is."""
+    none = _problem(sd, batch=0)
+    assert _attend(sd, "santa_decode_window", p=none, k=None, v=None) == sd.OK
+    assert _attend(sd, "santa_decode_kv4", p=none, kv4=None) == sd.OK
+    assert _attend(sd, "santa_decode_kv4", kv4=None) == sd.INVALID_ARG
+    for empty in (dict(total_tokens=0), dict(max_len=0)):  # refused before anything is enqueued, with the cache or not
+        assert _attend(sd, "santa_decode_kv4", p=_problem(sd, **empty), kv4=None, ws_bytes=0) == sd.WORKSPACE_TOO_SMALL
+        assert _attend(sd, "santa_decode_window", p=_problem(sd, **empty), k=None, v=None, ws_bytes=0) == sd.WORKSPACE_TOO_SMALL
