@@ -50,6 +50,14 @@ class Decoder:
         self._ws = {}
         self._prepare()
 
+    def __getstate__(self):
+        # references into the C structures stay behind: a copy makes its own
+        return {k: v for k, v in self.__dict__.items() if k not in ("_pref", "_windows")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._prepare()
+
     def workspace(self, mode: str) -> torch.Tensor:
         if mode not in self._ws:
             n = workspace_size(self.problem, MODES[mode])

@@ -203,3 +203,23 @@ def test_kv4_of_nothing_needs_no_cache(sd):
     for empty in (dict(total_tokens=0), dict(max_len=0)):  # refused before anything is enqueued, with the cache or not
         assert _attend(sd, "santa_decode_kv4", p=_problem(sd, **empty), kv4=None, ws_bytes=0) == sd.WORKSPACE_TOO_SMALL
         assert _attend(sd, "santa_decode_window", p=_problem(sd, **empty), k=None, v=None, ws_bytes=0) == sd.WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_decoder_can_be_copied_and_pickled(sd, how):
+    """A Decoder holds a problem and tensors, and goes where those go (to a worker process, into a checkpoint); the
+    copy's calls use the copy's problem."""
+    import copy
+    import pickle
+
+    from stochastic_sparse_decode_gb300.decoder import Decoder
+
+    dec = Decoder(2, 8, 2, 128, 4096, 2048, 256, 1, "bf16", device="cpu")
+    dec.workspace("prop")[0] = 7
+    dec._window(5, 1)
+    twin = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda x: pickle.loads(pickle.dumps(x))}[how](dec)
+    assert all(getattr(twin.problem, f) == getattr(dec.problem, f) for f, _ in dec.problem._fields_)
+    assert twin.device == dec.device and int(twin.workspace("prop")[0]) == 7
+    assert twin._pref._obj is twin.problem and twin._kv4_shape == dec._kv4_shape
+    with pytest.raises(ValueError):  # checked and refused as by the original: nothing lies on a CUDA device
+        twin.kv4_append(torch.zeros(4, 2, 128), torch.zeros(4, 2, 128), None, twin.kv4_cache())
