@@ -272,6 +272,7 @@ int run(int mode, int sampler, const santa_problem *p, const void *q, const void
     st = smem_check(p, mode, sampler, pages != nullptr);
     if (st != SANTA_OK) return st;
 
+    forget_error();
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const size_t n_out = size_t(p->batch) * p->num_q_heads * p->head_dim;
     if (L.Tmax == 0 || p->total_tokens == 0) {  // no sequence can hold a key
@@ -439,6 +440,7 @@ int santa_k_feature_blocked(const santa_problem *p, const void *k, void *k_fb, s
     if (need == 0) return SANTA_OK;
     if (!k || !k_fb || !aligned(k, 16) || !aligned(k_fb, 16)) return SANTA_INVALID_ARG;
     if (k_fb_bytes < need) return SANTA_WORKSPACE_TOO_SMALL;
+    forget_error();
     const cudaError_t e = launch_feature_block(p->dtype, k, k_fb, p->total_tokens, p->num_kv_heads, p->head_dim,
                                                reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SANTA_OK : SANTA_CUDA_ERROR;

@@ -10,6 +10,11 @@
 
 namespace santa {
 
+// Forgets an error that an earlier call of this thread left behind (a launch into an invalidated
+// capture, say, which that call reported): the entry points ask for the last error when they have
+// launched, and would report it a second time, for work that was enqueued as it should.
+inline void forget_error() { (void)cudaGetLastError(); }
+
 // Records the timing event `ev` (if any) on `stream`.  Inside stream capture it
 // becomes an event-record node of the graph, so a replayed graph is timed too.
 inline void record_event(cudaEvent_t ev, cudaStream_t stream) {

@@ -89,6 +89,7 @@ int attend(bool four_bit, const santa_problem *p, const santa_window *w, const s
     const SplitLayout L = split_layout(p);
     if (workspace_bytes < L.total) return SANTA_WORKSPACE_TOO_SMALL;
 
+    forget_error();
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (empty)
         return status(cudaMemsetAsync(out, 0, size_t(p->batch) * p->num_q_heads * p->head_dim * 4, stream));
@@ -173,6 +174,7 @@ int santa_page_plan(int batch, int page_size, int max_pages, long long num_pages
     if (!aligned(kv_lens, 4) || !aligned(new_lens, 4) || !aligned(page_table, 4) || !aligned(free_pages, 4) ||
         !aligned(slot_map, 16) || !aligned(positions, 16) || !aligned(lens_out, 4) || !aligned(counts, 4))
         return SANTA_INVALID_ARG;
+    forget_error();
     PlanParams pp = {batch,    page_size,  max_pages, num_free,  max_tokens, num_pages, kv_lens, new_lens,
                      free_pages, page_table, slot_map,  positions, lens_out,   counts,    err_word(dbg)};
     return status(launch_page_plan(pp, reinterpret_cast<cudaStream_t>(stream)));
@@ -200,6 +202,7 @@ int santa_norm_rope(const santa_problem *p, const santa_rope *r, int num_tokens,
     if (q && q == q_out && q_stride != (long long)p->num_q_heads * p->head_dim) return SANTA_INVALID_ARG;
     if (k && (k == k_cache || v == k_cache)) return SANTA_INVALID_ARG;  // rows move: not in place
     if (v && (v == v_cache || k == v_cache || k_cache == v_cache)) return SANTA_INVALID_ARG;
+    forget_error();
     RopeParams rp = {};
     rp.tokens = num_tokens;
     rp.Hq = p->num_q_heads;
@@ -245,6 +248,7 @@ int santa_kv4_append(const santa_problem *p, int num_tokens, const void *k, long
     if (!k || !v || !kv4 || !aligned(kv4, 16) || !aligned(slot_map, 8) || !rows_ok(k, k_stride, p->num_kv_heads, p) ||
         !rows_ok(v, v_stride, p->num_kv_heads, p))
         return SANTA_INVALID_ARG;
+    forget_error();
     StoreParams sp = {};
     sp.tokens = num_tokens;
     sp.Hkv = p->num_kv_heads;
@@ -268,6 +272,7 @@ int santa_kv4_read(const santa_problem *p, int num_tokens, const void *kv4, cons
     if (!kv4 || !aligned(kv4, 16) || !aligned(slot_map, 8) || !aligned(k, 16) || !aligned(v, 16) || k == v ||
         k == kv4 || v == kv4)
         return SANTA_INVALID_ARG;
+    forget_error();
     StoreParams sp = {};
     sp.tokens = num_tokens;
     sp.Hkv = p->num_kv_heads;
@@ -295,6 +300,7 @@ int santa_split_workspace_init(const santa_problem *p, void *workspace, size_t w
     if (!workspace || !aligned(workspace, 256)) return SANTA_INVALID_ARG;
     const SplitLayout L = split_layout(p);
     if (workspace_bytes < L.total) return SANTA_WORKSPACE_TOO_SMALL;
+    forget_error();
     return status(cudaMemsetAsync(workspace, 0, L.mz, reinterpret_cast<cudaStream_t>(stream)));
 }
 

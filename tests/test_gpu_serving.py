@@ -1138,3 +1138,53 @@ def test_attention_without_a_key_gives_zeros(kind, rows, max_len, page):
     out = torch.full((2, 4, 64), 7.0, device="cuda")
     _run_attention(kind, dec, q, [dec.kv4_cache()] if kind == "kv4" else pools, addr, page, 10, 2, out=out)
     assert not out.any()
+
+
+@pytest.mark.parametrize("name", ["window", "kv4", "norm_rope", "kv4_append", "kv4_read", "page_plan", "prop", "flash",
+                                  "exact", "feature_blocked"])
+def test_a_refused_call_is_reported_once(name):
+    """A call into a capture that another call has invalidated is refused by the launch; the next call, after the
+    capture's end, is not (the error that the first one left with the runtime is not its own)."""
+    import ctypes
+
+    c = _attention_case("window", "bf16", 128, 2, 4, [300, 40], 0, 0, 0, seed=80, poison=0.0)
+    k4 = _attention_case("kv4", "bf16", 128, 2, 4, [300, 40], 0, 0, 0, seed=80)
+    dec, q, (k, v), ind = c["dec"], c["q"], c["pools"], c["addr"]["indptr"]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n, rows = 5, dec.problem.total_tokens
+    U, cs = torch.full((2, 8), 0.3, device="cuda"), rope_table(400, 128)
+    x = torch.randn((n, 2, 128), device="cuda").bfloat16()
+    pos, slots = torch.arange(n, **i32), torch.arange(n, device="cuda")
+    out, new = torch.empty((2, 8, 128), device="cuda"), [torch.empty_like(x) for _ in range(2)]
+    plan = [torch.zeros(2, **i32), torch.full((2,), 2, **i32), torch.zeros((2, 3), **i32), torch.tensor([3, 1], **i32)]
+    got = [torch.empty(4, dtype=torch.int64, device="cuda"), torch.empty(4, **i32), torch.empty(2, **i32), torch.empty(2, **i32)]
+    stream = torch.cuda.Stream()
+    on = dict(stream=stream)
+    calls = {
+        "window": lambda: (dec.window(q, k, v, ind, 50, 3, out=out, **on),),
+        "kv4": lambda: (k4["dec"].kv4(q, k4["pools"][0], ind, out=out, **on),),
+        "norm_rope": lambda: (dec.norm_rope(None, x, x, pos, None, cs, *new, **on), *new)[1:],
+        "kv4_append": lambda: (dec.kv4_append(x, x, slots, k4["pools"][0], **on),),
+        "kv4_read": lambda: dec.kv4_read(k4["pools"][0], slots, *new, **on),
+        "page_plan": lambda: (dec.page_plan(plan[0], plan[1], plan[2], plan[3], 1, *got, **on), *got)[1:],
+        "feature_blocked": lambda: (dec.feature_blocked(k, **on),),
+        **{m: lambda m=m: (dec(m, q, k, v, ind, U, out=out, **on),) for m in ("prop", "flash", "exact")},
+    }
+    call = calls[name]
+    dec.workspace("prop"), dec.workspace("flash"), dec.workspace("exact")
+    torch.cuda.synchronize()
+    want = [t for t in call() if t is not None]
+    torch.cuda.synchronize()
+    want = [t.clone() for t in want]
+    torch.cuda.synchronize()
+    driver = ctypes.CDLL("libcuda.so.1")
+    handle, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+    assert driver.cuStreamBeginCapture_v2(handle, ctypes.c_int(2)) == 0
+    assert driver.cuStreamSynchronize(handle) != 0  # not allowed in a capture: invalidates it
+    with pytest.raises(sd.SantaError) as refused:
+        call()
+    assert driver.cuStreamEndCapture(handle, ctypes.byref(graph)) != 0 and not graph.value
+    assert refused.value.status == sd.CUDA_ERROR
+    again = [t for t in call() if t is not None]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, again)) and len(want) == len(again)
