@@ -1188,3 +1188,72 @@ def test_a_refused_call_is_reported_once(name):
     again = [t for t in call() if t is not None]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, again)) and len(want) == len(again)
+
+
+# ------------------------------------------------------------------------------ prompts through norm + rotation
+
+
+def _many_rows(tokens, heads, d):
+    """Whether a call has enough tokens for the kernels that keep several rows of a lane in flight (prompts)."""
+    parts = 1
+    while parts < heads and tokens * parts * (d // 8) < 152 * 640:
+        parts *= 2
+    return 4 * parts <= heads
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,hq,hkv,rot,inter,norm,form", [
+    (6500, 12, 4, 1.0, False, True, "fused"), (2500, 27, 9, 1.0, False, False, "fused"),
+    (2500, 27, 9, 0.5, False, True, "in place"), (6500, 12, 4, 0.25, False, False, "in place"),
+    (6500, 12, 4, 0.25, True, False, "fused"), (2500, 27, 9, 0.75, True, True, "in place"),
+    (12500, 3, 1, 1.0, False, True, "fused"), (12500, 3, 1, 0.5, True, False, "in place"),
+    (2500, 40, 1, 0.75, False, True, "fused"), (6500, 20, 2, 1.0, True, True, "q alone"),
+    (9000, 30, 30, 0.5, False, True, "k alone"),
+])
+def test_norm_rope_of_prompts(dtype, d, T, hq, hkv, rot, inter, norm, form):
+    """Both pairings, whole and partial rotations, with and without norms, q in place, one kind alone."""
+    dt = DT[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(T + hq)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    assert _many_rows(T, {"q alone": hq, "k alone": hkv}.get(form, hq + 2 * hkv), d)
+    if form == "fused":
+        qkv = rnd(T, hq + 2 * hkv + 1, d).to(dt)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:hq + 2 * hkv]
+    else:
+        q, k, v = (rnd(T, h, d).to(dt) for h in (hq, hkv, hkv))
+    rot, rows = int(rot * d), T + 9
+    cs = rope_table(5000, rot)
+    pos = torch.randint(0, 5000, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    slots = torch.randperm(rows, generator=gen, device="cuda")[:T].contiguous()
+    slots[::7] = -1  # padding
+    qw, kw = ((1 + 0.3 * rnd(d)).to(dt), (1 + 0.3 * rnd(d)).to(dt)) if norm else (None, None)
+    kc, vc = rnd(rows, hkv, d).to(dt), rnd(rows, hkv, d).to(dt)
+    kc0, vc0, q0 = kc.clone(), vc.clone(), q.clone()
+    dec = Decoder(1, hq, hkv, d, rows, rows, 256, 1, dtype)
+    dbg, word = _debug()
+    args = dict(interleaved=inter, eps=1e-5, debug=dbg)
+    if form == "q alone":
+        out = dec.norm_rope(q, None, None, pos, slots, cs, None, None, qw, kw, **args)
+    elif form == "k alone":
+        out = dec.norm_rope(None, k, None, pos, slots, cs, kc, None, qw, kw, **args)
+    else:
+        out = dec.norm_rope(q, k, v, pos, slots, cs, kc, vc, qw, kw, out=q if form == "in place" else None, **args)
+    assert _flags(word) == 0
+    angles = cs[pos.long()]
+    if out is not None:
+        want, mag = _rope_reference(q0, qw, 1e-5, angles, rot, inter)
+        _close(out, want, mag, "q")
+    live = slots >= 0
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[slots[live]] = False
+    if form != "q alone":
+        want, mag = _rope_reference(k, kw, 1e-5, angles, rot, inter)
+        _close(kc[slots[live]], want[live], mag[live], "k")
+    if not form.endswith("alone"):
+        assert torch.equal(vc[slots[live]], v[live])
+    else:
+        assert torch.equal(vc, vc0)
+    if form == "q alone":
+        assert torch.equal(kc, kc0)
+    assert torch.equal(kc[rest], kc0[rest]) and torch.equal(vc[rest], vc0[rest])
