@@ -1257,3 +1257,116 @@ def test_norm_rope_of_prompts(dtype, d, T, hq, hkv, rot, inter, norm, form):
     if form == "q alone":
         assert torch.equal(kc, kc0)
     assert torch.equal(kc[rest], kc0[rest]) and torch.equal(vc[rest], vc0[rest])
+
+
+# ------------------------------------------------------------------------------ a loop against the tokens' own history
+
+
+@pytest.mark.parametrize("kind", ["window", "kv4"])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_a_serving_loop_against_raw_tokens(kind, dtype, d):
+    """Prompts, then tokens one by one: pages and rows come from the plan's definition, keys and queries from the raw
+    tokens, normalised and rotated to their index in 64 bits.  Every row of the history is compared with the cache
+    after the last step, and each step's output with the attention over the history (in 4 bits: over what those rows
+    stand for).
+
+    The cache holds a rounding of each key, and q of each query, with the half step of its type, in front of which the
+    rotation errs by 24 u of a pair; in 4 bits a value is off by half a step of the group's scale and the roundings of
+    minimum and scale.  With dk and dq as those a logit is off by dx = |q| dk + dq (|k| + dk), and a weight by a factor
+    between exp(-2 max dx) and exp(2 max dx)."""
+    dt, B, hq, hkv, page, max_pages, num_pages = DT[dtype], 4, 6, 2, 32, 12, 64
+    gen = torch.Generator(device="cuda").manual_seed(90)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    half = torch.finfo(dt).eps / 2
+    dec = Decoder(B, hq, hkv, d, num_pages * page, max_pages * page, 256, 1, dtype)
+    cs = rope_table(max_pages * page, d)
+    qw, kw = ((1 + 0.3 * torch.randn(d, generator=gen, device="cuda")).to(dt) for _ in range(2))
+    k_pool, v_pool = (torch.full((num_pages * page, hkv, d), math.nan, device="cuda", dtype=dt) for _ in range(2))
+    kv4 = dec.kv4_cache().fill_(0xFF)  # NaN scales in every row that is not written
+    lens, table = torch.zeros(B, **i32), torch.full((B, max_pages), -1, **i32)
+    lens_h, table_h = np.zeros(B, np.int32), np.full((B, max_pages), -1, np.int32)
+    free_h = np.random.default_rng(2).permutation(num_pages).astype(np.int32)
+    hist = [dict(row=[], k=[], v=[]) for _ in range(B)]
+    window, sinks, scale = 45, 3, 1 / math.sqrt(d)
+
+    def record_error(x):
+        """How far a 4-bit record of x [..][d] may lie from it."""
+        g = (torch.arange(d, device="cuda") // 8) % (d // 64)
+        lo, hi = (torch.stack([f(x[..., g == j], -1) for j in range(d // 64)], -1)[..., g] for f in (torch.amin, torch.amax))
+        # scale and minimum are rounded to fp16 (2^-11), 15 scales between the extremes
+        return (hi - lo) / 15 * (0.5 + 16 * 2.0 ** -11) + 2.0 ** -11 * torch.maximum(lo.abs(), hi.abs()) + 2.0 ** -24
+
+    for step in range(5):
+        new = [50, 1, 33, 96] if step == 0 else [1, 1, 0, 1] if step == 2 else [1] * B
+        tokens = sum(new) + 2
+        qkv = torch.randn((tokens, hq + 2 * hkv, d), generator=gen, device="cuda").to(dt)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+        slots, pos = torch.empty(tokens, dtype=torch.int64, device="cuda"), torch.empty(tokens, **i32)
+        lens_out, counts = torch.empty(B, **i32), torch.empty(2, **i32)
+        dec.page_plan(lens, torch.tensor(new, **i32), table, torch.from_numpy(free_h).cuda(), page, slots, pos, lens_out, counts)
+        if kind == "kv4":
+            k_rot = k.new_empty(k.shape)
+            qr = dec.norm_rope(q, k, None, pos, None, cs, k_rot, None, qw, kw)
+            dec.kv4_append(k_rot, v, slots, kv4)
+        else:
+            qr = dec.norm_rope(q, k, v, pos, slots, cs, k_pool, v_pool, qw, kw)
+        table_h, slots_h, pos_h, lens_h, counts_h, flags = _plan_reference(lens_h, np.array(new, np.int32), table_h, free_h,
+                                                                           page, num_pages, tokens)
+        assert flags == 0
+        free_h, lens = free_h[counts_h[0]:], lens_out
+        t, last = 0, []
+        angles = cs[torch.from_numpy(pos_h).long().cuda()]
+        (kr, kmag), (qx, qmag) = (_rope_reference(x, w, 1e-6, angles, d, False) for x, w in ((k, kw), (q, qw)))
+        for b in range(B):
+            for _ in range(new[b]):
+                assert int(pos_h[t]) == len(hist[b]["row"])
+                hist[b]["row"].append(int(slots_h[t]))
+                hist[b]["k"].append((kr[t], half * kr[t].abs() + 24 * 2.0 ** -24 * kmag[t]))
+                hist[b]["v"].append(v[t].double())
+                t += 1
+            last.append(t - 1)  # the sequence's newest token (step 2: sequence 2 has none, its query is another's)
+        if step == 0:
+            continue
+        at = torch.tensor(last, device="cuda")
+        qs = qr[at].contiguous()
+        if kind == "kv4":
+            out = dec.kv4_paged(qs, kv4, table, lens, page, window, sinks)
+        else:
+            out = dec.window_paged(qs, k_pool, v_pool, table, lens, page, window, sinks)
+        assert lens.tolist() == lens_h.tolist() and torch.equal(table.cpu(), torch.from_numpy(table_h))
+        for b in range(B):
+            keep = _seen(len(hist[b]["row"]), window, sinks)
+            for h in range(hkv):
+                if kind == "kv4":
+                    kk, vv = _values64(kv4[torch.tensor(hist[b]["row"], device="cuda")[keep], h], d)
+                    dk = torch.zeros_like(kk)
+                else:
+                    kk, dk = (torch.stack([hist[b]["k"][i][j][h] for i in keep]) for j in range(2))
+                    vv = torch.stack([hist[b]["v"][i][h] for i in keep])
+                heads = slice(3 * h, 3 * h + 3)
+                qq = qx[at[b], heads]
+                dq = half * qq.abs() + 24 * 2.0 ** -24 * qmag[at[b], heads]
+                want, tol = _attention_reference(qq, kk, vv, scale, 2.0 ** -22)
+                p = torch.softmax(qq @ kk.T * scale, -1)
+                dx = (qq.abs() @ dk.T + dq @ (kk.abs() + dk).T) * scale
+                tol = tol + torch.expm1(2 * dx.amax(-1, keepdim=True)) * (p @ vv.abs())
+                err = (out[b, heads].double() - want).abs()
+                assert (err <= tol).all(), (step, b, h, float((err / tol).max()))
+    for b in range(B):
+        rows = torch.tensor(hist[b]["row"], device="cuda")
+        kk, dk = (torch.stack([x[j] for x in hist[b]["k"]]) for j in range(2))
+        vv = torch.stack(hist[b]["v"])
+        if kind == "kv4":
+            got_k, got_v = _values64(kv4[rows], d)
+            assert ((got_v - vv).abs() <= record_error(vv)).all()
+            # of the rounded key, whose group's extremes may lie dk further out
+            dk = dk + record_error(kk) + 2 / 15 * dk.amax(-1, keepdim=True)
+        else:
+            got_k = k_pool[rows].double()
+            assert torch.equal(v_pool[rows].double(), vv)
+        assert ((got_k - kk).abs() <= dk).all()
+    used = torch.tensor(sorted({r for x in hist for r in x["row"]}), device="cuda")
+    rest = torch.ones(num_pages * page, dtype=torch.bool, device="cuda")
+    rest[used] = False
+    assert len(used) == sum(len(x["row"]) for x in hist)
+    assert (kv4[rest] == 0xFF).all() and k_pool[rest].isnan().all() and v_pool[rest].isnan().all()
