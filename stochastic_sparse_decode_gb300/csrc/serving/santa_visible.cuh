@@ -1,5 +1,5 @@
 // santa_visible.cuh -- which keys a decode query sees: the first `sinks` of its sequence
-// and the last `window` (visible index j -> key j for j < s, else lo + j - s).
+// and the last `window`.
 #pragma once
 
 #include "santa_serving.h"
@@ -10,8 +10,6 @@ struct Visible {
     int L;   // keys of the sequence
     int s;   // visible sinks
     int lo;  // first key of the window, >= s
-    __device__ __forceinline__ int count() const { return s + L - lo; }
-    __device__ __forceinline__ int key(int j) const { return j < s ? j : lo + j - s; }
 };
 __device__ __forceinline__ Visible visible(int L, int window, int sinks) {
     Visible v;
