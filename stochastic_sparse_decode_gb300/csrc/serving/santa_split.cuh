@@ -41,6 +41,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// An 8 x 8 matrix of 16-bit elements, two per lane, transposed over the warp.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // A head of the walk: the visible blocks of (sequence b, KV head kvh), units u0 .. u0 + nb - 1.
 struct Head {
     int b, kvh, nb;

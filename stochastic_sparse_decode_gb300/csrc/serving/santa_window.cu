@@ -34,12 +34,6 @@ namespace santa {
 
 namespace {
 
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
 // (x, y) as three bf16 pairs whose sum is (x, y) to 2^-24 relative.
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
 #pragma unroll
