@@ -367,6 +367,15 @@ __global__ void __launch_bounds__(ExactStreamGeom<T, D, G>::kWarps * 32, 1)
             // heads >= G zero) from the score array, split into bf16 high and low
             // parts so that e keeps ~16 bits.  Keys past the chunk's end have e = 0.
             if (len > 0) {
+                if (len < kChunkRows) {  // the rows behind them hold anything: zeros (0 x NaN is NaN)
+                    for (int i = lane; i < (kChunkRows - len) * Geo::kBoxes * 8; i += 32) {
+                        const int r = len + (i >> 3) / Geo::kBoxes, bx = (i >> 3) % Geo::kBoxes;
+                        *reinterpret_cast<uint4 *>(vbuf + bx * kChunkBoxBytes + r * 128 + (i & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();  // before the next copy into this buffer
+                    __syncwarp();
+                }
                 const int g = lane >> 2, t = lane & 3, mq = lane >> 3, mi = lane & 7;
                 uint32_t bh[2][2], bl[2][2];
 #pragma unroll

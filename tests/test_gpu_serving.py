@@ -1370,3 +1370,30 @@ def test_a_serving_loop_against_raw_tokens(kind, dtype, d):
     rest[used] = False
     assert len(used) == sum(len(x["row"]) for x in hist)
     assert (kv4[rest] == 0xFF).all() and k_pool[rest].isnan().all() and v_pool[rest].isnan().all()
+
+
+@pytest.mark.parametrize("garbage", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,d,g", [("bf16", 128, 4), ("bf16", 64, 8), ("bf16", 128, 1), ("f32", 64, 2)])
+def test_exact_decode_sees_no_row_behind_the_sequence(dtype, d, g, garbage):
+    """The block of 32 rows that holds a sequence's last keys goes on into the rows behind it (the next sequence's, or
+    those of a cache that is not full): whatever they hold, exact_decode gives the same bits."""
+    lens, hkv, dt = [1, 45, 64, 31, 333], 2, DT[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(100)
+    gap = 40  # rows between the sequences: kv_indptr leaves none out, so a sequence of garbage stands there
+    starts, at = [], 0
+    for n in lens:
+        starts += [at, at + n]
+        at += n + gap
+    rows = at + 5
+    k, v = (torch.randn((rows, hkv, d), generator=gen, device="cuda").to(dt) for _ in range(2))
+    B = 2 * len(lens)  # every second sequence is a gap
+    ind = torch.tensor(starts + [at], device="cuda")
+    q = torch.randn((B, hkv * g, d), generator=gen, device="cuda").to(dt)
+    dec = Decoder(B, hkv * g, hkv, d, rows, 400, 256, 1, dtype)
+    want = dec("exact", q, k, v, ind)
+    for i, n in enumerate(lens):
+        for x in (k, v):
+            x[starts[2 * i + 1]:starts[2 * i + 1] + gap] = garbage
+    k[at:], v[at:] = garbage, garbage
+    got = dec("exact", q, k, v, ind)
+    assert torch.isfinite(want).all() and torch.equal(got[::2], want[::2])
