@@ -563,9 +563,12 @@ int santa_kv4_read(const santa_problem *p, int num_tokens, const void *kv4, cons
 
 /*
  * Exact decode attention over the 4-bit cache: santa_decode_window's arguments with
- * kv4 for k and v; w may be NULL (all keys).  The problem's dtype is q's.  The
- * dequantised values enter as they stand (no rounding to 8 or 16 bits); q, the
- * softmax weights and the sums keep 22 bits or more.
+ * kv4 for k and v; w may be NULL (all keys).  The problem's dtype is q's, its
+ * elements below 2^100.  The dequantised values enter as they stand (no rounding to 8
+ * or 16 bits); the sums are fp32; q keeps 22 bits against the largest element of its
+ * head, a weight times its value's scale 22 bits until it lies 2^17 below the largest
+ * scale among the keys that it is summed with, and fewer below that (its error is
+ * never above 2^-39 of that scale).
  */
 int santa_decode_kv4(const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
                      const void *kv4, const long long *kv_indptr, float *out, void *workspace,

@@ -38,13 +38,20 @@
 // d = 64: a record is 72 bytes, which TMA's strides cannot express; the codes go from global
 // memory to registers, the next block's while the current one is computed.
 //
-// Bound by instructions: about 790 per warp and block of 32 keys, 0.57 issued per cycle and
-// scheduler by 4 warps of 128 registers.  16 sequences of 32768 tokens, 32 query and 8 KV heads
-// of 128 (604 MB): 138 us = 4.4 TB/s, 0.64 of the copy rate (the same walk without arithmetic: 98
-// us); one such sequence 22.2 us.  On the way, for the 16: one warp per key in fp32 4612 us;
-// tensor cores on converted registers 199; q and the weights as the A operand 197; codes as the
-// A operand with the heads twice 132, centred 155, one LOP3 per pair 147, K as subnormals 138.
-// 12 warps of 168 registers: 218 us at the 132 step.
+// Bound by instructions: about 800 per warp and block of 32 keys, 0.58 issued per cycle and
+// scheduler by 4 warps of 128 registers (which d = 128 with up to four heads in bf16 exceeds: 88
+// bytes of spill stores, 68 paged).  16 sequences of 32768 tokens, 32 query and 8 KV heads of 128
+// (604 MB): 138 us = 4.4 TB/s, 0.64 of the copy rate (the same walk without arithmetic: 98 us).  On
+// the way, for the 16: one warp per key in fp32 4612 us; tensor cores on converted registers 199; q
+// and the weights as the A operand 197; codes as the A operand with the heads twice 132, centred
+// 155, one LOP3 per pair 147, K as subnormals 138.  12 warps of 168 registers: 218 us at the 132
+// step; so are the shapes that 16 warps do not fit, five to eight heads (shared memory) 216 us and
+// fp32 queries (registers of their second part, and its products) 212.  d = 64: 96 us for half the
+// bytes, as scales, softmax and weights are work per key.  1000 sequences of 100 keys: 74 us, work
+// per head (four units each).
+// One sequence of 32768 (22.2 us): lengths and plan 1.7 us, the first blocks of all warps, 11 MB
+// at once, 4, three or four blocks a warp 8, join within the CTA 2.2, count 1, parts 5 (device
+// timestamps).
 #include <cuda_fp16.h>
 
 #include "santa_split.cuh"

@@ -14,10 +14,13 @@
 // further than 1e-5 from the middle between two codes rounds as the quotient does.
 //
 // A prompt of 8191 tokens, 8 heads of 128, is 43 MB in and out for either direction (6.3 us at
-// the copy rate).  Both are bound by instructions: 14 us and 9 us (2.8 and 4.5 TB/s), at first
-// 22 each.  What brought them down: two blocks per lane instead of one (20 -> 15 and 12 -> 9.5),
-// packed minimum and maximum, no IEEE division, rounding and packing by the low bits of a large
-// float, and codes read as fp16 subnormals.  Two or four rows in flight per lane: no gain.
+// the copy rate): 15.0 us and 9.4 us (2.9 and 4.6 TB/s), at first 22 each.  Neither is bound by one
+// thing: the warps' 9.8 and 5.0 million instructions are 7.8 and 4.0 us of every scheduler's time at
+// the top clock, 0.59 and 0.58 of the cycles issue one, and half (append) or more (read) of a
+// warp's time between two of them is the wait for its loads.  What brought them down: two blocks per lane instead
+// of one (20 -> 15 and 12 -> 9.5), packed minimum and maximum, no IEEE division, rounding and packing
+// by the low bits of a large float, and codes read as fp16 subnormals.  Two or four rows in flight
+// per lane were tried and brought no gain.
 #include <cuda_fp16.h>
 
 #include "santa_rows.cuh"

@@ -14,8 +14,8 @@
 // turn (queries, then keys, then values), kMany of them in flight; when there are not enough
 // tokens to fill the GPU so, every lane row takes one row, and a warp passes by the kinds that
 // it has no row of (one row per lane at 8191 tokens: 54 us; kMany at 777 tokens of 24 fp32 rows of
-// 64: 8.3 us against 3.1).  8191 tokens, 32 query and 8 KV heads of 128 in bf16, 206 MB: 35.4 us =
-// 5.8 TB/s, 0.85 of the copy rate.
+// 64: 8.3 us against 3.1).  8191 tokens, 32 query and 8 KV heads of 128 in bf16, 206 MB: 35.2 us =
+// 5.8 TB/s, 0.86 of the copy rate.
 #include "santa_rows.cuh"
 #include "santa_serving.h"
 

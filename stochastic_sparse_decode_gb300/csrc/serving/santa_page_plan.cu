@@ -14,8 +14,10 @@
 // entries that another CTA writes are never read.
 //
 // Bound by latency: lengths, two scans and a search precede the first store.  64 sequences of
-// one token each 4.2 us; 200 prompts of 4096 tokens on average (9.8 MB written, 1.5 us at the
-// copy rate) 8.4 us, 12.5 with a search and scalar stores per token.
+// one token each 4.1 us; 200 prompts of 4096 tokens on average (9.8 MB written, 1.5 us at the
+// copy rate) 8.3 us, 12.5 with a search and scalar stores per token.  The prompts' 4.0 million
+// warp instructions are 3.2 us of every scheduler's time, by under 4 warps each that issue in 0.42 of
+// the cycles: the part behind the scans is instructions as much as it is latency.
 #include "santa_serving.h"
 
 namespace santa {

@@ -28,7 +28,8 @@ namespace santa {
 constexpr int kBlock = 32;         // keys per unit
 constexpr int kMinUnitsPerCta = 4; // fewer CTAs than the grid has while a CTA would get less
 // Joining a head's parts across CTAs costs about as much as a CTA's reading of this many
-// units (4 us; a unit adds 0.14 to 0.16 us to a CTA's time, bf16 or 4-bit, d = 128).  So when
+// units (4 us; a unit adds 0.14 to 0.16 us to a CTA's time, bf16 or 4-bit, d = 128; other
+// dimensions and fp32 were not measured for this choice).  So when
 // the heads are no more than the CTAs, each takes one head whole unless the longest head is
 // longer than this and an equal share of all units together.  Batch 1, 8 KV heads, bf16, whole
 // against split: 256 keys 6.2 / 8.9 us, 768 8.9 / 9.4, 1024 10.2 / 9.6, 2048 15.0 / 9.9; batch

@@ -21,10 +21,12 @@
 // the tensor cores' additions truncate, and a chain over thousands of keys would drift.
 //
 // Bound by memory where there is enough of it: 64 ragged sequences of 4096 to 32768 tokens,
-// window 4096 and 4 sinks (1.07 GB of K and V), 176 us = 6.1 TB/s, 0.90 of the copy rate; 12
-// warps with one K and one V buffer each keep 196 KB in flight per SM.  One sequence (16.8 MB)
-// takes 10.9 us, a chain of dependent steps: lengths and plan 1.5 us, first K and V 1.5,
-// weights and sums 1, join within the CTA 1, count 1.5, parts 2 (device timestamps).
+// window 4096 and 4 sinks (1.07 GB of K and V), 173 us = 6.2 TB/s, 0.92 of the copy rate; 12
+// warps with one K and one V buffer each keep 196 KB in flight per SM.  At d = 64 that is half as
+// much, and 16 sequences of 16384 keys take 126 us, 0.62 of the copy rate.  One sequence (16.8 MB)
+// takes 10.6 us, a chain of dependent steps: lengths and plan 1.7 us, first K 0.8, first V 0.8,
+// weights and sums 0.8, the last warp 0.3, join within the CTA 1.6, count 1, parts 3 (device
+// timestamps, which add up to 10.0).
 // fp32: a lane forms the whole dot products of one key (rows read along the swizzle
 // without bank conflicts), then owns d / 32 dimensions of the sums.
 #include "santa_split.cuh"
