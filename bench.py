@@ -167,11 +167,17 @@ def measured_peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
-def source_digest() -> str:
-    """Digest of the device code (the kernels live in the .cuh headers and .cu files)."""
+def source_digest(serving: bool = False) -> str:
+    """Digest of the device code (the kernels live in the .cuh headers and .cu files) of the decode modes, or,
+    with ``serving``, of the operators around them: csrc/serving and the headers that those include."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "stochastic_sparse_decode_gb300", "csrc")
-    for f in sorted(glob.glob(os.path.join(csrc, "*.cuh")) + glob.glob(os.path.join(csrc, "*.cu"))):
+    files = glob.glob(os.path.join(csrc, "*.cuh"))
+    if serving:
+        files += glob.glob(os.path.join(csrc, "*.h")) + glob.glob(os.path.join(csrc, "serving", "*"))
+    else:
+        files += glob.glob(os.path.join(csrc, "*.cu"))
+    for f in sorted(files):
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())
             h.update(fh.read())

@@ -223,3 +223,32 @@ def test_decoder_can_be_copied_and_pickled(sd, how):
     assert twin._pref._obj is twin.problem and twin._kv4_shape == dec._kv4_shape
     with pytest.raises(ValueError):  # checked and refused as by the original: nothing lies on a CUDA device
         twin.kv4_append(torch.zeros(4, 2, 128), torch.zeros(4, 2, 128), None, twin.kv4_cache())
+
+
+def test_profiles_were_taken_on_these_sources(tmp_path, monkeypatch):
+    """Every summary under profiles/ states the digest of the kernel sources that it describes, and the digest changes
+    with any of their files."""
+    import shutil
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, root)
+    import bench
+
+    serving = ("kv4_", "window_", "page_plan")
+    for f in sorted(os.listdir(os.path.join(root, "profiles"))):
+        text = open(os.path.join(root, "profiles", f)).read()
+        stated = re.search(r"- source_digest: `([0-9a-f]{16})`", text).group(1)
+        assert stated == bench.source_digest(serving=f.startswith(serving)), f
+    csrc = os.path.join("stochastic_sparse_decode_gb300", "csrc")
+    shutil.copytree(os.path.join(root, csrc), tmp_path / csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    before = {k: bench.source_digest(serving=k) for k in (False, True)}
+    for name, changes in (("serving/santa_split.cuh", {True}), ("serving/santa_kv4_attn.cu", {True}),
+                          ("serving/santa_serving.h", {True}), ("santa_launch.h", {True}),
+                          ("santa_common.cuh", {False, True}), ("santa_prop.cu", {False})):
+        path = tmp_path / csrc / name
+        old = path.read_bytes()
+        path.write_bytes(old + b"\n")
+        assert {k for k in before if bench.source_digest(serving=k) != before[k]} == changes, name
+        path.write_bytes(old)
