@@ -574,6 +574,114 @@ int santa_decode_kv4(const santa_problem *p, const santa_window *w, const santa_
                      const void *kv4, const long long *kv_indptr, float *out, void *workspace,
                      size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream);
 
+/* Which axis turns which pair, for santa_norm_rope_axes. */
+typedef struct {
+    int axes;                 /* position axes, 1 .. 4 (time, height and width, say) */
+    long long axis_stride;    /* positions of axis a begin at positions + a axis_stride; >= num_tokens */
+    unsigned char axis[64];   /* axis of pair i, i < rot_dim / 2, each below `axes` */
+} santa_axes;
+
+/*
+ * santa_norm_rope for tokens that have a position on each of several axes (the time,
+ * row and column of an image's or a video's patch; text has the same number on all of
+ * them): pair i of token t turns by the angle of column i of the table's row
+ * positions[axis[i]][t].  The table's columns are free, so axes with frequencies of
+ * their own (axis a's first pair fastest) are a matter of the table.  positions:
+ * device [axes] rows of num_tokens int32; each is checked as in santa_norm_rope.
+ * Every other argument, and the results where all axes agree, are santa_norm_rope's.
+ */
+int santa_norm_rope_axes(const santa_problem *p, const santa_rope *r, const santa_axes *axes, int num_tokens,
+                         const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
+                         long long v_stride, const int *positions, const long long *slot_map, void *q_out,
+                         void *k_cache, void *v_cache, const santa_debug *dbg, santa_stream_t stream);
+
+/* The keys that all sequences of a batch see before their own. */
+typedef struct {
+    int len;                  /* keys of the prefix, >= 0 */
+    long long start;          /* its first cache row (contiguous cache); ignored with pages */
+} santa_prefix;
+
+/*
+ * Exact decode attention for a batch that shares a prefix: out_b = softmax over the
+ * prefix's keys and sequence b's own, as if each had a copy, but the prefix is read
+ * once for the whole batch: the queries of all sequences (batch * Hq / Hkv rows per KV
+ * head) are multiplied with its keys and values together.
+ *   contiguous  the prefix is the rows start .. start + len - 1, kv_indptr gives each
+ *               sequence's own rows (max_len bounds those)
+ *   pages       every sequence's page-table row begins with the prefix's pages, and
+ *               kv_lens counts the prefix too (max_len >= len bounds it).  The prefix's
+ *               pages are read from sequence 0's row.  len need not be a multiple of the
+ *               page size.  A sequence with kv_lens[b] < len has no keys of its own: it
+ *               sees the prefix alone.  kv_indptr is unused
+ * What rows behind the prefix or behind a sequence hold does not matter; a page id
+ * outside [0, num_pages) drops that page's keys and raises SANTA_ERR_INDPTR.  A sequence
+ * that sees no key gives zeros.  Equal calls give equal bits.  Sequences that share
+ * different prefixes are calls of their own (on slices of q, page_table, kv_lens, out).
+ * Single precision throughout: a weight keeps 24 bits on the tensor cores too.
+ * Workspace: santa_shared_workspace_size, prepared once by santa_split_workspace_init;
+ * rules and the other arguments as for santa_decode_window.
+ */
+int santa_decode_shared(const santa_problem *p, const santa_prefix *prefix, const santa_pages *pages, const void *q,
+                        const void *k, const void *v, const long long *kv_indptr, float *out, void *workspace,
+                        size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream);
+int santa_shared_workspace_size(const santa_problem *p, size_t *bytes);
+
+/*
+ * The attention weight that every cached key has received.  scores is [Hkv][total_tokens]
+ * float32, a plane per KV head indexed by cache row.  For key i of sequence b at cache
+ * row r, with A the softmax of each query head of the group,
+ *   scores_out[h][r] = decay * scores[h][r] + sum over the group's heads of A_i,
+ * where the last `fresh` keys of a sequence start from 0 (their rows may hold another
+ * token's score).  Rows of no sequence are left as they are.  scores may be scores_out,
+ * or NULL (all start from 0).
+ *   q, k given   pass 1 of santa_decode_prop runs first, on workspace; of K alone is read
+ *   both NULL    workspace is as santa_prop_pass1 left it for the same problem and
+ *                kv_indptr (not with pages): a sampled decode gets the weights between
+ *                its passes, without another read of K
+ * Either way the workspace is left as santa_prop_pass1 leaves it: ready for
+ * santa_prop_pass2 or another call of this function, and for other prop calls after
+ * santa_workspace_init.  Workspace: santa_workspace_size with SANTA_MODE_PROP, and
+ * that mode's limits (Hq / Hkv in {1, 2, 4, 8}, max_len <= 2^22).  decay >= 0, finite.
+ */
+int santa_key_weights(const santa_problem *p, const santa_pages *pages, const void *q, const void *k,
+                      const long long *kv_indptr, const float *scores, float *scores_out, float decay, int fresh,
+                      void *workspace, size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream);
+
+/* What santa_evict keeps of each sequence, per KV head. */
+typedef struct {
+    int sinks;                /* the first keys, >= 0 */
+    int recent;               /* the last keys, >= 0 */
+    int budget;               /* of those between, as many of the highest scores, >= 0 */
+} santa_keep;
+
+/*
+ * Eviction by score: of every sequence and KV head the first `sinks` keys, the last
+ * `recent` and the `budget` keys of highest score among the others (ties: the lowest
+ * index; a NaN counts as lower than every number) are copied, in the order of the
+ * sequence, to the first rows of that sequence in another cache.  All heads keep the
+ * same number, lens_out[b] = min(L_b, sinks + recent + budget), but not the same keys.
+ *   scores        device [Hkv][total_tokens] float32 (santa_key_weights)
+ *   kv_indptr, pages          where the sequences lie, as for santa_decode_window
+ *   k_out, v_out  [rows_out][Hkv][d]; they may be k and v themselves (one page pool)
+ *                 when the rows written belong to no sequence read
+ *   scores_out    [Hkv][rows_out], or NULL: the scores move with the keys.  Not scores
+ *   indptr_out    device [B+1] int64: sequence b goes to the rows from indptr_out[b] on
+ *                 (at least lens_out[b] of them); unused with pages_out
+ *   pages_out     the page-table rows that receive the sequences (kv_lens is unused;
+ *                 num_pages * page_size == rows_out); NULL: contiguous
+ *   kept          device [B][Hkv][sinks + recent + budget] int32: the index that each
+ *                 row held before, -1 behind the last
+ *   lens_out      device [B] int32
+ * A destination that does not fit (a bad page id, or an indptr_out entry without room)
+ * is not written, and raises SANTA_ERR_INDPTR; a key on a bad source page counts as of
+ * lowest score and its row is not written.  Rows behind a sequence's last are left as
+ * they are.  Two kernels, no workspace.
+ */
+int santa_evict(const santa_problem *p, const santa_keep *keep, const santa_pages *pages, const void *k, const void *v,
+                const float *scores, const long long *kv_indptr, void *k_out, void *v_out, float *scores_out,
+                long long rows_out, const long long *indptr_out, const santa_pages *pages_out, int *kept,
+                int *lens_out, const santa_debug *dbg, santa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -50,6 +50,11 @@ EXPORTS = (
     "santa_kv4_append",
     "santa_kv4_read",
     "santa_decode_kv4",
+    "santa_norm_rope_axes",
+    "santa_decode_shared",
+    "santa_shared_workspace_size",
+    "santa_key_weights",
+    "santa_evict",
     "santa_status_string",
 )
 
@@ -125,6 +130,24 @@ class Window(ctypes.Structure):
     _fields_ = [("window", ctypes.c_int), ("sinks", ctypes.c_int)]
 
 
+class Axes(ctypes.Structure):
+    """santa_axes"""
+
+    _fields_ = [("axes", ctypes.c_int), ("axis_stride", ctypes.c_longlong), ("axis", ctypes.c_ubyte * 64)]
+
+
+class Prefix(ctypes.Structure):
+    """santa_prefix"""
+
+    _fields_ = [("len", ctypes.c_int), ("start", ctypes.c_longlong)]
+
+
+class Keep(ctypes.Structure):
+    """santa_keep"""
+
+    _fields_ = [("sinks", ctypes.c_int), ("recent", ctypes.c_int), ("budget", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -164,6 +187,12 @@ def lib() -> ctypes.CDLL:
         L.santa_kv4_size.argtypes = [P, ctypes.POINTER(sz)]
         L.santa_kv4_append.argtypes = [P, i, vp, ll, vp, ll, vp, vp, Dp, vp]
         L.santa_kv4_read.argtypes = [P, i, vp, vp, vp, vp, Dp, vp]
+        L.santa_norm_rope_axes.argtypes = [P, ctypes.POINTER(Rope), ctypes.POINTER(Axes), i, vp, ll, vp, ll, vp, ll, vp, vp,
+                                           vp, vp, vp, Dp, vp]
+        L.santa_decode_shared.argtypes = [P, ctypes.POINTER(Prefix), Gp, vp, vp, vp, vp, vp, vp, sz, Dp, vp]
+        L.santa_shared_workspace_size.argtypes = [P, ctypes.POINTER(sz)]
+        L.santa_key_weights.argtypes = [P, Gp, vp, vp, vp, vp, vp, ctypes.c_float, i, vp, sz, Dp, vp]
+        L.santa_evict.argtypes = [P, ctypes.POINTER(Keep), Gp, vp, vp, vp, vp, vp, vp, vp, ll, vp, Gp, vp, vp, Dp, vp]
         L.santa_read_device_error.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint)]
         L.santa_status_string.argtypes = [ctypes.c_int]
         L.santa_status_string.restype = ctypes.c_char_p
@@ -379,6 +408,47 @@ def santa_norm_rope(problem, rope, q, k, v, positions, slot_map, q_out, k_cache,
     _check("santa_norm_rope", lib().santa_norm_rope(
         ctypes.byref(problem), ctypes.byref(rope), n, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
         _ptr(positions), _ptr(slot_map), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ref(debug), _stream(stream)))
+
+
+def santa_norm_rope_axes(problem, rope, axes, q, k, v, positions, slot_map, q_out, k_cache, v_cache, debug=None,
+                         stream=None):
+    """santa_norm_rope with a position per axis (axes: an Axes; positions [axes][tokens]): see santa_decode.h."""
+    n = next((int(t.shape[0]) for t in (q, k, v) if t is not None), 0)
+    strides = [0 if t is None else _row_stride(t) for t in (q, k, v)]
+    _check("santa_norm_rope_axes", lib().santa_norm_rope_axes(
+        ctypes.byref(problem), ctypes.byref(rope), ctypes.byref(axes), n, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
+        strides[2], _ptr(positions), _ptr(slot_map), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ref(debug),
+        _stream(stream)))
+
+
+def shared_workspace_size(problem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("santa_shared_workspace_size", lib().santa_shared_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return n.value
+
+
+def santa_decode_shared(problem, prefix, q, k, v, kv_indptr, out, workspace, pages=None, debug=None, stream=None):
+    """Exact decode for a batch that shares a prefix (prefix: a Prefix): see santa_decode.h."""
+    _check("santa_decode_shared", lib().santa_decode_shared(
+        ctypes.byref(problem), ctypes.byref(prefix), _ref(pages), _ptr(q), _ptr(k), _ptr(v), _ptr(kv_indptr), _ptr(out),
+        _ptr(workspace), _nbytes(workspace), _ref(debug), _stream(stream)))
+
+
+def santa_key_weights(problem, q, k, kv_indptr, scores, scores_out, decay, fresh, workspace, pages=None, debug=None,
+                      stream=None):
+    """Adds the keys' attention weights to their scores (workspace: a prop workspace): see santa_decode.h."""
+    _check("santa_key_weights", lib().santa_key_weights(
+        ctypes.byref(problem), _ref(pages), _ptr(q), _ptr(k), _ptr(kv_indptr), _ptr(scores), _ptr(scores_out), float(decay),
+        int(fresh), _ptr(workspace), _nbytes(workspace), _ref(debug), _stream(stream)))
+
+
+def santa_evict(problem, keep, k, v, scores, kv_indptr, k_out, v_out, scores_out, indptr_out, kept, lens_out, pages=None,
+                pages_out=None, debug=None, stream=None):
+    """Copies what is kept by score into another cache (keep: a Keep): see santa_decode.h."""
+    _check("santa_evict", lib().santa_evict(
+        ctypes.byref(problem), ctypes.byref(keep), _ref(pages), _ptr(k), _ptr(v), _ptr(scores), _ptr(kv_indptr),
+        _ptr(k_out), _ptr(v_out), _ptr(scores_out), int(k_out.shape[0]), _ptr(indptr_out), _ref(pages_out), _ptr(kept),
+        _ptr(lens_out), _ref(debug), _stream(stream)))
 
 
 def santa_page_plan(page_size, num_pages, kv_lens, new_lens, page_table, free_pages, slot_map, positions, lens_out,

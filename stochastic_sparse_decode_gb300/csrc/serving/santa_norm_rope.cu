@@ -108,8 +108,10 @@ __device__ __forceinline__ void take_rows(const T *src, T *dst, const T *weight,
 }
 
 // A lane row takes the rows part, part + parts, ... of one token's Hq queries, Hkv keys and Hkv values.
-template <typename T, int D, bool kInter, int kAhead>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_kernel(const RopeParams p, int parts) {
+// kAxes: a position per axis, and an axis per pair (two bits each, the lane's four in axis4[l]).
+template <typename T, int D, bool kInter, int kAhead, bool kAxes>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 3)
+    norm_rope_kernel(const __grid_constant__ RopeParams p, int parts) {
     constexpr int kL = D / 8;
     const int l = threadIdx.x % kL;
     const long long row = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / kL;
@@ -124,23 +126,44 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 3) norm_rop
     pdl_wait();
     pdl_launch_dependents();
 
-    int pos = load(p.positions + t);
-    if (pos < 0 || pos >= p.max_pos) {
-        if (p.err && live) atomicOr(p.err, SANTA_ERR_POSITION);
-        pos = pos < 0 ? 0 : p.max_pos - 1;
-    }
+    auto checked = [&](int pos) {
+        if (pos < 0 || pos >= p.max_pos) {
+            if (p.err && live) atomicOr(p.err, SANTA_ERR_POSITION);
+            pos = pos < 0 ? 0 : p.max_pos - 1;
+        }
+        return pos;
+    };
     long long slot = p.slot_map ? load(p.slot_map + t) : t;
     if (slot >= p.total_tokens) {
         if (p.err && live) atomicOr(p.err, SANTA_ERR_SLOT);
         slot = -1;
     }
     float c[4] = {}, s[4] = {};
-    if (turns) {
-        const float *cs = p.cos_sin + (size_t)pos * p.rot_dim + 4 * l;
-        const float4 u = load(reinterpret_cast<const float4 *>(cs));
-        const float4 v = load(reinterpret_cast<const float4 *>(cs + p.rot_dim / 2));
-        c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w;
-        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+    if constexpr (kAxes) {
+        int pos[4] = {};
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+            if (a < p.axes) pos[a] = checked(load(p.positions + a * p.axis_stride + t));
+        if (turns) {
+            const float *cs = p.cos_sin + 4 * l;
+            const unsigned ax = p.axis4[l];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned a = ax >> (2 * j) & 3;
+                const float *at = cs + (size_t)(a < 2 ? a == 0 ? pos[0] : pos[1] : a == 2 ? pos[2] : pos[3]) * p.rot_dim + j;
+                c[j] = load(at);
+                s[j] = load(at + p.rot_dim / 2);
+            }
+        }
+    } else {
+        const int pos = checked(load(p.positions + t));
+        if (turns) {
+            const float *cs = p.cos_sin + (size_t)pos * p.rot_dim + 4 * l;
+            const float4 u = load(reinterpret_cast<const float4 *>(cs));
+            const float4 v = load(reinterpret_cast<const float4 *>(cs + p.rot_dim / 2));
+            c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w;
+            s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+        }
     }
     const int nq = p.q ? p.Hq : 0, nk = p.k ? p.Hkv : 0, nv = p.v ? p.Hkv : 0;
     // row r of the token goes to part r mod parts, counted through q, k and v
@@ -179,17 +202,20 @@ cudaError_t launch_norm_rope(const RopeParams &p, int dtype, int d, cudaStream_t
     auto go = [&](auto kern) {
         return launch_kernel(kern, dim3(unsigned(ctas)), dim3(kRopeThreads), 0, stream, true, 0, false, p, parts);
     };
-    auto pick = [&](auto inter, auto ahead) {
-        constexpr bool kInter = decltype(inter)::value;
+    auto pick = [&](auto inter, auto ahead, auto axes) {
+        constexpr bool kInter = decltype(inter)::value, kAx = decltype(axes)::value;
         constexpr int kA = decltype(ahead)::value;
         if (dtype == SANTA_BF16)
-            return d == 128 ? go(norm_rope_kernel<uint16_t, 128, kInter, kA>) : go(norm_rope_kernel<uint16_t, 64, kInter, kA>);
-        return d == 128 ? go(norm_rope_kernel<float, 128, kInter, kA>) : go(norm_rope_kernel<float, 64, kInter, kA>);
+            return d == 128 ? go(norm_rope_kernel<uint16_t, 128, kInter, kA, kAx>)
+                            : go(norm_rope_kernel<uint16_t, 64, kInter, kA, kAx>);
+        return d == 128 ? go(norm_rope_kernel<float, 128, kInter, kA, kAx>) : go(norm_rope_kernel<float, 64, kInter, kA, kAx>);
     };
-    const std::integral_constant<int, 1> a1;
-    const std::integral_constant<int, kMany> a4;
-    if (p.interleaved) return one ? pick(std::true_type(), a1) : pick(std::true_type(), a4);
-    return one ? pick(std::false_type(), a1) : pick(std::false_type(), a4);
+    auto pick_ahead = [&](auto inter, auto axes) {
+        return one ? pick(inter, std::integral_constant<int, 1>(), axes) : pick(inter, std::integral_constant<int, kMany>(), axes);
+    };
+    if (p.axes)
+        return p.interleaved ? pick_ahead(std::true_type(), std::true_type()) : pick_ahead(std::false_type(), std::true_type());
+    return p.interleaved ? pick_ahead(std::true_type(), std::false_type()) : pick_ahead(std::false_type(), std::false_type());
 }
 
 }  // namespace santa

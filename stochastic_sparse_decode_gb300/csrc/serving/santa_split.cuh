@@ -60,7 +60,7 @@ struct Head {
     __device__ __forceinline__ int first_key(int n) const { return kBlock * (n < nsb ? n : wb0 + n - nsb); }
 };
 __device__ __forceinline__ void set_blocks(Head &h, int L, const SplitParams &sp) {
-    h.vis = visible(L, sp.window, sp.sinks);
+    h.vis = visible(L, sp.window, sp.sinks, sp.first);
     h.nsb = (h.vis.s + kBlock - 1) / kBlock;
     h.wb0 = h.vis.lo / kBlock;
     if (h.wb0 < h.nsb || h.vis.lo >= L) {  // the two meet, or all keys are sinks
@@ -171,7 +171,11 @@ __device__ __forceinline__ unsigned seen_bits(const Walk &w) {
     return __ballot_sync(kFull, w.row >= 0 && key < v.L && (key < v.s || key >= v.lo));
 }
 
-__device__ __forceinline__ void zero_row(const Params &p, int b) {
+// The row of a sequence without a key.
+__device__ __forceinline__ void zero_row(const SplitParams &sp, int b) {
+    const Params &p = sp.p;
+    if (sp.own_mz)
+        for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) sp.own_mz[size_t(b) * p.Hq + i] = make_float2(-INFINITY, 0.f);
     float4 *o = reinterpret_cast<float4 *>(p.out + size_t(b) * p.Hq * p.D);
     for (int i = threadIdx.x; i < p.Hq * p.D / 4; i += blockDim.x) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
@@ -222,7 +226,7 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                 while (empty) {
                     const int e = 32 * k + __ffs(empty) - 1;
                     empty &= empty - 1;
-                    if (e % gridDim.x == blockIdx.x) zero_row(p, e);
+                    if (e % gridDim.x == blockIdx.x) zero_row(sp, e);
                 }
                 int v = nb[k];
 #pragma unroll
@@ -334,7 +338,7 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                  e += gridDim.x) {
                 Head g;
                 load_head<kPaged>(g, sp, e);
-                if (g.nb == 0) zero_row(p, e);
+                if (g.nb == 0) zero_row(sp, e);
             }
         }
         __syncthreads();
@@ -452,6 +456,7 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
         const float Z = warp_sum(in ? sh.Z[lane][h] * c : 0.f);
         if (u0 >= cta0 && u0 + sh.nb[i] <= cta1) {  // nobody else has a part
             c = Z == 0.f ? 0.f : c / Z;
+            if (sp.own_mz && lane == 0) sp.own_mz[size_t(sh.b[i]) * p.Hq + sh.kvh[i] * G + h] = make_float2(M, Z);
         } else if (lane == 0) {
             const int part = u0 <= cta0 ? 0 : 1;
             __stcg(sp.part_mz + (size_t(blockIdx.x) * 2 + part) * G + h, make_float2(M, Z));
@@ -547,6 +552,8 @@ __device__ __forceinline__ void join_pieces(const SplitParams &sp, SplitShared<N
                 }
                 Z = warp_sum(Z);
                 const float inv = Z == 0.f ? 0.f : 1.f / Z;
+                if (sp.own_mz && lane == 0)
+                    sp.own_mz[size_t(sh.inc_b[k]) * p.Hq + sh.inc_kvh[k] * G + h] = make_float2(M, Z);
 #pragma unroll
                 for (int u = 0; u < kPer; ++u) {
                     const int c = lane + 32 * u;

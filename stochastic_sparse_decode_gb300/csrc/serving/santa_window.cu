@@ -153,9 +153,13 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                         dst[16 * m + g] = Ot[m][j] * f;
                         dst[16 * m + 8 + g] = Ot[m][2 + j] * f;
                     }
-                    if (!final && g == 0) {
-                        sh.M[slot][h] = M[j];
-                        sh.Z[slot][h] = Z[j];
+                    if (g == 0) {
+                        if (!final) {
+                            sh.M[slot][h] = M[j];
+                            sh.Z[slot][h] = Z[j];
+                        } else if (sp.own_mz) {
+                            sp.own_mz[size_t(head.b) * p.Hq + head.kvh * G + h] = make_float2(M[j], Z[j]);
+                        }
                     }
                 }
             }
@@ -168,9 +172,13 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                     const float f = !final ? 1.f : z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
                     for (int e = 0; e < kE; ++e) dst[lane * kE + e] = O[h][e] * f;
-                    if (!final && lane == 0) {
-                        sh.M[slot][h] = M[h];
-                        sh.Z[slot][h] = z;
+                    if (lane == 0) {
+                        if (!final) {
+                            sh.M[slot][h] = M[h];
+                            sh.Z[slot][h] = z;
+                        } else if (sp.own_mz) {
+                            sp.own_mz[size_t(head.b) * p.Hq + head.kvh * G + h] = make_float2(M[h], z);
+                        }
                     }
                 }
         }

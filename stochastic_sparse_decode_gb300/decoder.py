@@ -15,9 +15,10 @@ import ctypes
 
 import torch
 
-from . import (BF16, MODES, Debug, Pages, Rope, Window, _check, _stream, decode, k_feature_blocked_size, kv4_size, lib,
-               make_pages, make_problem, santa_decode_prop_bernoulli, santa_decode_prop_paged, santa_k_feature_blocked,
-               santa_prop_pass1, santa_prop_pass2, split_workspace_size, workspace_size)
+from . import (BF16, MODE_PROP, MODES, Axes, Debug, Keep, Pages, Prefix, Rope, Window, _check, _stream, decode,
+               k_feature_blocked_size, kv4_size, lib, make_pages, make_problem, santa_decode_prop_bernoulli,
+               santa_decode_prop_paged, santa_k_feature_blocked, santa_prop_pass1, santa_prop_pass2, shared_workspace_size,
+               split_workspace_size, workspace_size)
 
 _F32, _I32, _I64, _U8 = (frozenset((t,)) for t in (torch.float32, torch.int32, torch.int64, torch.uint8))
 
@@ -40,6 +41,26 @@ def rope_table(max_pos, rot_dim, theta=10000.0, device="cuda") -> torch.Tensor:
     return torch.cat([ang.cos(), ang.sin()], 1).to(torch.float32)
 
 
+def rope_sections(sections) -> tuple:
+    """The axis of each pair where the axes take runs of pairs, one after another: sections (16, 24, 24) give pairs
+    0 .. 15 to axis 0, the next 24 to axis 1 and the last 24 to axis 2."""
+    return tuple(a for a, n in enumerate(sections) for _ in range(n))
+
+
+def rope_turns(pairs, axes) -> tuple:
+    """The axis of each pair where the axes take the pairs in turn: 0, 1, 2, 0, 1, 2, ..."""
+    return tuple(i % axes for i in range(pairs))
+
+
+def rope_table_axes(max_pos, sections, theta=10000.0, device="cuda") -> torch.Tensor:
+    """cos_sin of santa_norm_rope_axes for axes with frequencies of their own: within the run of a section of n pairs
+    (rope_sections), pair i turns by theta^(-i / n) per position.  (rope_table serves axes that share the frequencies
+    of one table.)"""
+    freq = torch.cat([float(theta) ** (-torch.arange(n, dtype=torch.float64, device=device) / n) for n in sections if n])
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([ang.cos(), ang.sin()], 1).to(torch.float32)
+
+
 class Decoder:
     def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, total_tokens, max_len, tile, S, dtype,
                  device=None):
@@ -52,7 +73,7 @@ class Decoder:
 
     def __getstate__(self):
         # references into the C structures stay behind: a copy makes its own
-        return {k: v for k, v in self.__dict__.items() if k not in ("_pref", "_windows")}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_pref", "_windows", "_axes")}
 
     def __setstate__(self, state):
         self.__dict__.update(state)
@@ -156,6 +177,7 @@ class Decoder:
         self._kv4_shape = (p.total_tokens, p.num_kv_heads, p.head_dim + p.head_dim // 8)
         self._pref = ctypes.byref(p)
         self._windows = {}
+        self._axes = {}
 
     def _refuse(self, name, t, dtypes, shape, dev, how=""):
         """Says why a tensor that the C call would misread is refused: dtype, shape (None: any size), device,
@@ -185,13 +207,24 @@ class Decoder:
     def split_workspace(self) -> torch.Tensor:
         """The workspace of window and kv4 calls (kept; calls that overlap need a Decoder each).  The first use
         prepares it, which a stream capture would only record: call this before capturing."""
-        if "split" not in self._ws:
+        return self._zeroed("split", "split_workspace()", lambda: split_workspace_size(self.problem))
+
+    def shared_workspace(self) -> torch.Tensor:
+        """The workspace of shared and shared_paged, under the rules of split_workspace."""
+        return self._zeroed("shared", "shared_workspace()", lambda: shared_workspace_size(self.problem))
+
+    def weights_workspace(self) -> torch.Tensor:
+        """The workspace of key_weights and key_weights_paged, under the rules of split_workspace."""
+        return self._zeroed("weights", "weights_workspace()", lambda: workspace_size(self.problem, MODE_PROP))
+
+    def _zeroed(self, key, how, size) -> torch.Tensor:
+        if key not in self._ws:
             if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("the workspace must exist before a capture: call split_workspace() first")
+                raise RuntimeError(f"the workspace must exist before a capture: call {how} first")
             # zero-filled: what santa_split_workspace_init does; complete before a call on any stream
-            self._ws["split"] = torch.zeros(split_workspace_size(self.problem), dtype=torch.uint8, device=self.device)
-            torch.cuda.current_stream(self._ws["split"].device).synchronize()
-        return self._ws["split"]
+            self._ws[key] = torch.zeros(size(), dtype=torch.uint8, device=self.device)
+            torch.cuda.current_stream(self._ws[key].device).synchronize()
+        return self._ws[key]
 
     def _window(self, window, sinks):
         if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
@@ -199,6 +232,28 @@ class Decoder:
         if len(self._windows) >= 64:
             self._windows.clear()
         return self._windows.setdefault((window, sinks), ctypes.byref(Window(window, sinks)))
+
+    def _where(self, kv_indptr, pages, dev):
+        """(address of kv_indptr, pages): one of them None."""
+        p = self.problem
+        if pages is None:
+            if not _fits(kv_indptr, _I64, (p.batch + 1,), dev):
+                self._refuse("kv_indptr", kv_indptr, _I64, (p.batch + 1,), dev)
+            return kv_indptr.data_ptr(), None
+        table, lens, size = pages
+        if table.dim() != 2 or not _fits(table, _I32, (p.batch, table.shape[1]), dev):
+            self._refuse("page_table", table, _I32, (p.batch, None), dev)
+        if not _fits(lens, _I32, (p.batch,), dev):
+            self._refuse("kv_lens", lens, _I32, (p.batch,), dev)
+        if size < 1 or p.total_tokens % size:
+            raise ValueError(f"page_size {size} does not divide total_tokens {p.total_tokens}")
+        return None, ctypes.byref(Pages(table.data_ptr(), lens.data_ptr(), size, table.shape[1], p.total_tokens // size))
+
+    def _on(self, ws, dev):
+        """A workspace's address; its device must be the tensors'."""
+        if ws.get_device() != dev:
+            raise ValueError(f"the tensors are on CUDA device {dev}, this Decoder's workspace on {ws.device}")
+        return ws.data_ptr()
 
     def _attend(self, kind, q, k, v, kv_indptr, pages, window, sinks, out, debug, stream):
         dev = q.get_device()
@@ -210,21 +265,7 @@ class Decoder:
                     self._refuse(name, t, self._dt, self._kv_shape, dev)
         elif not _fits(k, _U8, self._kv4_shape, dev):
             self._refuse("kv4", k, _U8, self._kv4_shape, dev)
-        p = self.problem
-        indptr = pref = None
-        if pages is None:
-            if not _fits(kv_indptr, _I64, (p.batch + 1,), dev):
-                self._refuse("kv_indptr", kv_indptr, _I64, (p.batch + 1,), dev)
-            indptr = kv_indptr.data_ptr()
-        else:
-            table, lens, size = pages
-            if table.dim() != 2 or not _fits(table, _I32, (p.batch, table.shape[1]), dev):
-                self._refuse("page_table", table, _I32, (p.batch, None), dev)
-            if not _fits(lens, _I32, (p.batch,), dev):
-                self._refuse("kv_lens", lens, _I32, (p.batch,), dev)
-            if size < 1 or p.total_tokens % size:
-                raise ValueError(f"page_size {size} does not divide total_tokens {p.total_tokens}")
-            pref = ctypes.byref(Pages(table.data_ptr(), lens.data_ptr(), size, table.shape[1], p.total_tokens // size))
+        indptr, pref = self._where(kv_indptr, pages, dev)
         out = self._out(out, dev)
         w = self._windows.get((window, sinks))
         if w is None:
@@ -264,6 +305,145 @@ class Decoder:
                   stream=None) -> torch.Tensor:
         """The same on a paged 4-bit cache."""
         return self._attend("kv4", q, kv4, None, None, (page_table, kv_lens, page_size), window, sinks, out, debug, stream)
+
+    def _shared(self, q, k, v, kv_indptr, pages, start, prefix_len, out, debug, stream):
+        dev = q.get_device()
+        if not _fits(q, self._dt, self._q_shape, dev):
+            self._refuse("q", q, self._dt, self._q_shape, dev)
+        for name, t in (("k", k), ("v", v)):
+            if not _fits(t, self._dt, self._kv_shape, dev):
+                self._refuse(name, t, self._dt, self._kv_shape, dev)
+        if not (0 <= prefix_len < 1 << 31 and 0 <= start < 1 << 31):
+            raise ValueError(f"start {start}, prefix_len {prefix_len}: whole numbers from 0 to 2^31 - 1 are needed")
+        indptr, pref = self._where(kv_indptr, pages, dev)
+        out = self._out(out, dev)
+        ws = self._ws.get("shared")
+        if ws is None:
+            ws = self.shared_workspace()
+        _check("santa_decode_shared", lib().santa_decode_shared(
+            self._pref, ctypes.byref(Prefix(prefix_len, start)), pref, q.data_ptr(), k.data_ptr(), v.data_ptr(), indptr,
+            out.data_ptr(), self._on(ws, dev), ws.numel(), None if debug is None else ctypes.byref(debug),
+            self._stream(dev, stream)))
+        return out
+
+    def shared(self, q, k, v, kv_indptr, start, prefix_len, out=None, debug=None, stream=None) -> torch.Tensor:
+        """Exact decode for a batch whose sequences all see the rows start .. start + prefix_len - 1 of the cache
+        before their own, kv_indptr's (santa_decode_shared): the prefix is read once for the batch."""
+        return self._shared(q, k, v, kv_indptr, None, start, prefix_len, out, debug, stream)
+
+    def shared_paged(self, q, k_pool, v_pool, page_table, kv_lens, page_size, prefix_len, out=None, debug=None,
+                     stream=None) -> torch.Tensor:
+        """The same on a paged cache: every row of page_table begins with the prefix's pages, kv_lens counts it too."""
+        return self._shared(q, k_pool, v_pool, None, (page_table, kv_lens, page_size), 0, prefix_len, out, debug, stream)
+
+    def _plane(self, name, t, rows, dev):
+        shape = (self.problem.num_kv_heads, rows)
+        if not _fits(t, _F32, shape, dev):
+            self._refuse(name, t, _F32, shape, dev)
+        return t.data_ptr()
+
+    def _key_weights(self, q, k, kv_indptr, pages, scores, out, decay, fresh, debug, stream):
+        p = self.problem
+        dev = (out if scores is None else scores).get_device() if scores is not None or out is not None else q.get_device()
+        if (q is None) != (k is None):
+            raise ValueError("q and k are both given, or both left out after pass1")
+        if q is not None:
+            if not _fits(q, self._dt, self._q_shape, dev):
+                self._refuse("q", q, self._dt, self._q_shape, dev)
+            if not _fits(k, self._dt, self._kv_shape, dev):
+                self._refuse("k", k, self._dt, self._kv_shape, dev)
+        indptr, pref = self._where(kv_indptr, pages, dev)
+        if out is None:
+            out = scores if scores is not None else torch.zeros((p.num_kv_heads, p.total_tokens), device=dev)
+        sp = None if scores is None else self._plane("scores", scores, p.total_tokens, dev)
+        op = self._plane("out", out, p.total_tokens, dev)
+        if not 0 <= fresh < 1 << 31:
+            raise ValueError(f"fresh {fresh}: a whole number from 0 to 2^31 - 1 is needed")
+        if q is None:
+            ws = self._ws.get("prop")
+            if ws is None:
+                raise ValueError("without q and k, pass1 must have run on this Decoder's workspace")
+        else:
+            ws = self._ws.get("weights")
+            if ws is None:
+                ws = self.weights_workspace()
+        _check("santa_key_weights", lib().santa_key_weights(
+            self._pref, pref, None if q is None else q.data_ptr(), None if k is None else k.data_ptr(), indptr, sp, op,
+            decay, fresh, self._on(ws, dev), ws.numel(), None if debug is None else ctypes.byref(debug),
+            self._stream(dev, stream)))
+        return out
+
+    def key_weights(self, q, k, kv_indptr, scores=None, out=None, decay=1.0, fresh=0, debug=None,
+                    stream=None) -> torch.Tensor:
+        """out [Hkv][total_tokens] = decay * scores + the attention weight that each key receives from the group's
+        queries (santa_key_weights); without `out`, scores is updated in place.  The last `fresh` keys of a sequence
+        start from 0.  q and k None: after pass1 and before pass2, from what pass1 left."""
+        return self._key_weights(q, k, kv_indptr, None, scores, out, decay, fresh, debug, stream)
+
+    def key_weights_paged(self, q, k_pool, page_table, kv_lens, page_size, scores=None, out=None, decay=1.0, fresh=0,
+                          debug=None, stream=None) -> torch.Tensor:
+        """The same on a paged cache (with q and k)."""
+        if q is None or k_pool is None:
+            raise ValueError("a paged cache needs q and k")
+        return self._key_weights(q, k_pool, None, (page_table, kv_lens, page_size), scores, out, decay, fresh, debug, stream)
+
+    def _evict(self, k, v, scores, kv_indptr, pages, sinks, recent, budget, k_out, v_out, scores_out, indptr_out, table_out,
+               kept, lens_out, debug, stream):
+        p, dev = self.problem, k.get_device()
+        for name, t in (("k", k), ("v", v)):
+            if not _fits(t, self._dt, self._kv_shape, dev):
+                self._refuse(name, t, self._dt, self._kv_shape, dev)
+        rows = k_out.shape[0]
+        shape = (rows, p.num_kv_heads, p.head_dim)
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if not _fits(t, self._dt, shape, dev):
+                self._refuse(name, t, self._dt, shape, dev)
+        sp = self._plane("scores", scores, p.total_tokens, dev)
+        op = None if scores_out is None else self._plane("scores_out", scores_out, rows, dev)
+        if min(sinks, recent, budget) < 0 or sinks + recent + budget >= 1 << 31:
+            raise ValueError(f"sinks {sinks}, recent {recent}, budget {budget}: whole numbers below 2^31 together are needed")
+        indptr, pref = self._where(kv_indptr, pages, dev)
+        to = pout = None
+        if table_out is None:
+            if not _fits(indptr_out, _I64, (p.batch + 1,), dev):
+                self._refuse("indptr_out", indptr_out, _I64, (p.batch + 1,), dev)
+            to = indptr_out.data_ptr()
+        else:
+            size = pages[2]
+            if table_out.dim() != 2 or not _fits(table_out, _I32, (p.batch, table_out.shape[1]), dev):
+                self._refuse("page_table_out", table_out, _I32, (p.batch, None), dev)
+            if rows % size:
+                raise ValueError(f"page_size {size} does not divide the {rows} rows of k_out")
+            pout = ctypes.byref(Pages(table_out.data_ptr(), None, size, table_out.shape[1], rows // size))
+        shape = (p.batch, p.num_kv_heads, sinks + recent + budget)
+        if kept is None:
+            kept = torch.empty(shape, dtype=torch.int32, device=dev)
+        elif not _fits(kept, _I32, shape, dev):
+            self._refuse("kept", kept, _I32, shape, dev)
+        if lens_out is None:
+            lens_out = torch.empty(p.batch, dtype=torch.int32, device=dev)
+        elif not _fits(lens_out, _I32, (p.batch,), dev):
+            self._refuse("lens_out", lens_out, _I32, (p.batch,), dev)
+        _check("santa_evict", lib().santa_evict(
+            self._pref, ctypes.byref(Keep(sinks, recent, budget)), pref, k.data_ptr(), v.data_ptr(), sp, indptr,
+            k_out.data_ptr(), v_out.data_ptr(), op, rows, to, pout, kept.data_ptr(), lens_out.data_ptr(),
+            None if debug is None else ctypes.byref(debug), self._stream(dev, stream)))
+        return kept, lens_out
+
+    def evict(self, k, v, scores, kv_indptr, sinks, recent, budget, k_out, v_out, scores_out, indptr_out, kept=None,
+              lens_out=None, debug=None, stream=None):
+        """Copies, per sequence and KV head, the first `sinks` keys, the last `recent` and the `budget` of highest
+        score between them to the rows from indptr_out[b] on of k_out and v_out (santa_evict).  Returns (kept
+        [B][Hkv][sinks + recent + budget], the index that each row held before, and lens_out [B])."""
+        return self._evict(k, v, scores, kv_indptr, None, sinks, recent, budget, k_out, v_out, scores_out, indptr_out, None,
+                           kept, lens_out, debug, stream)
+
+    def evict_paged(self, k_pool, v_pool, scores, page_table, kv_lens, page_size, sinks, recent, budget, k_out, v_out,
+                    scores_out, page_table_out, kept=None, lens_out=None, debug=None, stream=None):
+        """The same from a paged cache into the pages of page_table_out (of page_size rows, in the pools k_out and
+        v_out, which may be k_pool and v_pool)."""
+        return self._evict(k_pool, v_pool, scores, None, (page_table, kv_lens, page_size), sinks, recent, budget, k_out,
+                           v_out, scores_out, None, page_table_out, kept, lens_out, debug, stream)
 
     def kv4_cache(self) -> torch.Tensor:
         """An empty 4-bit cache for the problem's total_tokens: [rows][Hkv][d + d / 8] bytes."""
@@ -336,10 +516,41 @@ class Decoder:
         k_cache, or v with v_cache may be None.  Without a slot map token t goes to row t, and k_cache and v_cache
         may also be [tokens][Hkv][d], with at most total_tokens tokens: the rotated keys by themselves, as
         kv4_append takes them."""
+        return self._norm_rope(q, k, v, positions, None, slot_map, cos_sin, k_cache, v_cache, q_weight, k_weight, eps,
+                               interleaved, out, debug, stream)
+
+    def norm_rope_axes(self, q, k, v, positions, axis, slot_map, cos_sin, k_cache, v_cache, q_weight=None, k_weight=None,
+                       eps=1e-6, interleaved=False, out=None, debug=None, stream=None):
+        """norm_rope with a position on each of several axes (santa_norm_rope_axes): positions is [axes][tokens], and
+        axis[i] is the axis of pair i (rope_sections, rope_turns, or any sequence of rot_dim / 2 whole numbers)."""
+        return self._norm_rope(q, k, v, positions, axis, slot_map, cos_sin, k_cache, v_cache, q_weight, k_weight, eps,
+                               interleaved, out, debug, stream)
+
+    def _axes_of(self, axis, axes, stride):
+        if len(self._axes) >= 64:
+            self._axes.clear()
+        if not 1 <= len(axis) <= 64 or not all(0 <= a < axes for a in axis):
+            raise ValueError(f"axis: up to 64 whole numbers below the {axes} rows of positions are needed")
+        return self._axes.setdefault((axis, axes, stride),
+                                     ctypes.byref(Axes(axes, stride, (ctypes.c_ubyte * 64)(*axis))))
+
+    def _norm_rope(self, q, k, v, positions, axis, slot_map, cos_sin, k_cache, v_cache, q_weight, k_weight, eps,
+                   interleaved, out, debug, stream):
         p, dev = self.problem, positions.get_device()
-        n, d = positions.shape[0], p.head_dim
-        if not _fits(positions, _I32, (n,), dev):
-            self._refuse("positions", positions, _I32, (None,), dev)
+        n, d = positions.shape[-1], p.head_dim
+        if axis is None:
+            if not _fits(positions, _I32, (n,), dev):
+                self._refuse("positions", positions, _I32, (None,), dev)
+        else:
+            rows = positions.shape[0]
+            if positions.dtype not in _I32 or positions.dim() != 2 or (n > 1 and positions.stride(1) != 1) or (
+                    rows > 1 and positions.stride(0) < n):
+                self._refuse("positions", positions, _I32, (None, None), dev)
+            axis = tuple(axis)
+            at = (axis, rows, positions.stride(0) if rows > 1 else n)
+            axes = self._axes.get(at) or self._axes_of(*at)
+            if len(axis) * 2 != cos_sin.shape[-1]:
+                raise ValueError(f"axis: {len(axis)} pairs, cos_sin has {cos_sin.shape[-1] // 2}")
         if cos_sin.dim() != 2 or not _fits(cos_sin, _F32, cos_sin.shape, dev):
             self._refuse("cos_sin", cos_sin, _F32, (None, None), dev)
         qp = kp = vp = op = kc = vc = qw = kw = None
@@ -373,9 +584,12 @@ class Decoder:
                 self._refuse("k_weight", k_weight, self._dt, (d,), dev)
             kw = k_weight.data_ptr()
         r = Rope(qw, kw, eps, cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], bool(interleaved))
-        _check("santa_norm_rope", lib().santa_norm_rope(
-            self._pref, ctypes.byref(r), n, qp, qs, kp, ks, vp, vs, positions.data_ptr(), self._slots(slot_map, n, dev), op,
-            kc, vc, None if debug is None else ctypes.byref(debug), self._stream(dev, stream)))
+        st, dbg = self._stream(dev, stream), None if debug is None else ctypes.byref(debug)
+        args = (n, qp, qs, kp, ks, vp, vs, positions.data_ptr(), self._slots(slot_map, n, dev), op, kc, vc, dbg, st)
+        if axis is None:
+            _check("santa_norm_rope", lib().santa_norm_rope(self._pref, ctypes.byref(r), *args))
+        else:
+            _check("santa_norm_rope_axes", lib().santa_norm_rope_axes(self._pref, ctypes.byref(r), axes, *args))
         return out
 
     def page_plan(self, kv_lens, new_lens, page_table, free_pages, page_size, slot_map, positions, lens_out, counts,
