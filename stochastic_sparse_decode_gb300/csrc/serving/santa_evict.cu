@@ -4,9 +4,10 @@
 // Kept are the first `sinks` keys, the last `recent`, and of the n between the k = budget of
 // highest score (ties: lowest index).  The k-th highest is found digit by digit (11, 11 and 10
 // bits from the top) on the scores as unsigned numbers of the same order: a histogram of the
-// digit over the keys that agree with the digits found so far, and the bin in which the count
-// from the top passes k.  No sort, and the work does not depend on k.  The scores lie in shared
-// memory from the first pass on (up to kCached keys; those beyond are read again).
+// digit, and the bin in which the count from the top passes k.  The keys of the first digit's bin
+// are listed, and the other two digits look at that list alone.  No sort, and the work does not
+// depend on k.  The scores lie in shared memory from the first digit on (up to kCached keys; those
+// beyond are read again), the list takes up to kListed of them.
 // Then every warp counts the keys of its stretch above the threshold and equal to it, one scan
 // over the warps places them, and the indices are written in order.
 // The move is a second kernel over all SMs: `rows` destination rows of all KV heads per CTA,
@@ -18,9 +19,10 @@ namespace santa {
 namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = 32;
-constexpr int kCached = 49152;  // scores held in shared memory
+constexpr int kCached = 40960;  // scores held in shared memory
+constexpr int kListed = 8192;   // keys of one bin that are listed; more are looked for among all
 constexpr int kBins = 2048;
-constexpr size_t kSelSmem = size_t(kCached) * 4 + kBins * 4;
+constexpr size_t kSelSmem = size_t(kCached + kListed + kBins) * 4;
 
 // Scores as unsigned numbers of the same order; -0 is 0, a NaN 0 (below every number).
 __device__ __forceinline__ unsigned ordered(float x) {
@@ -34,8 +36,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kvh = blockIdx.x, b = blockIdx.y;
     extern __shared__ __align__(16) unsigned char smem[];
-    unsigned *hist = reinterpret_cast<unsigned *>(smem), *cache = hist + kBins;
-    __shared__ unsigned warp_sum_[kSelWarps], found[2];
+    unsigned *hist = reinterpret_cast<unsigned *>(smem), *list = hist + kBins, *cache = list + kListed;
+    __shared__ unsigned warp_sum_[kSelWarps], found[2], listed;
     __shared__ int warp_n[2][kSelWarps];
     pdl_wait();
     pdl_launch_dependents();
@@ -50,96 +52,150 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
         for (int i = threadIdx.x; i < n_out; i += kSelThreads) kept[i] = i;
         return;
     }
+    for (int i = threadIdx.x; i < lo; i += kSelThreads) kept[i] = i;
+    for (int i = threadIdx.x; i < L - hi; i += kSelThreads) kept[lo + k + i] = hi + i;
+    if (k == 0) return;
+    // the blocks of 32 keys that hold the middle; a warp takes a stretch of them
     const float *scores = e.scores + size_t(kvh) * p.total_tokens;
-    auto fetch = [&](int i) {  // key lo + i
-        const long long row = key_row<kPaged>(p, b, start, lo + i);
+    const int first = lo / 32, blocks = (hi + 31) / 32 - first, seg = (blocks + kSelWarps - 1) / kSelWarps;
+    const int s0 = min(blocks, warp * seg), s1 = min(blocks, s0 + seg);
+    auto inside = [&](int i) {  // key i of the middle's blocks
+        const int key = first * 32 + i;
+        return key >= lo && key < hi;
+    };
+    auto row_of = [&](int blk) {  // its first cache row, -1: a bad page (a block lies on one page)
+        return blk < s1 ? key_row<kPaged>(p, b, start, (first + blk) * 32) : -1LL;
+    };
+    auto value = [&](int i) {
+        if (i < kCached) return cache[i];
+        if (!inside(i)) return 0u;
+        const long long row = key_row<kPaged>(p, b, start, first * 32 + i);
         return row < 0 ? 0u : ordered(load(scores + row));
     };
+    // counts one key of a bin; a warp that agrees (many equal scores) counts once
+    auto count = [&](bool in, unsigned bin) {
+        int same;
+        __match_all_sync(kFull, in ? bin : 0xffffffffu, &same);
+        if (same) {
+            if (in && lane == 0) atomicAdd(hist + bin, 32u);
+        } else if (in) {
+            atomicAdd(hist + bin, 1u);
+        }
+    };
+    auto clear = [&]() {
+        for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+        if (threadIdx.x == 0) listed = 0;
+        __syncthreads();
+    };
     unsigned prefix = 0, left = unsigned(k);  // the digits found; keys still to take among those that share them
-    if (k > 0) {
+    auto find = [&](int shift) {
+        __syncthreads();
+        // counts from the top: thread t holds bins 2047 - 2t and 2046 - 2t
+        const unsigned h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
+        unsigned s = h0 + h1;
 #pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-            for (int base = 0; base < n; base += kSelThreads * 4) {
-                unsigned v[4];
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned t = __shfl_up_sync(kFull, s, o);
+            if (lane >= o) s += t;
+        }
+        if (lane == 31) warp_sum_[warp] = s;
+        __syncthreads();
+        unsigned sums = warp_sum_[lane];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = base + u * kSelThreads + threadIdx.x;
-                    v[u] = i >= n ? 0u : pass && i < kCached ? cache[i] : fetch(i);
-                }
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned t = __shfl_up_sync(kFull, sums, o);
+            if (lane >= o) sums += t;
+        }
+        const unsigned through = __shfl_sync(kFull, sums, warp), before = through - warp_sum_[warp] + s - h0 - h1;
+        if (before < left && left <= before + h0 + h1) {  // one thread's
+            const bool second = left > before + h0;
+            found[0] = unsigned(kBins - 1 - 2 * threadIdx.x) - (second ? 1u : 0u);
+            found[1] = left - before - (second ? h0 : 0u);
+        }
+        __syncthreads();
+        prefix |= found[0] << shift;
+        left = found[1];
+    };
+    clear();
+    for (int base = s0; base < s1; base += 32) {
+        const long long rows = row_of(base + lane);  // of 32 blocks, a lane each
+        const int m = min(32, s1 - base);
+        constexpr int kAhead = 8;
+        for (int j = 0; j < m; j += kAhead) {
+            float x[kAhead];
+            bool ok[kAhead];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = base + u * kSelThreads + threadIdx.x;
-                    if (pass == 0 && i < n && i < kCached) cache[i] = v[u];
-                    const bool in = i < n && (pass == 0 || (v[u] >> (shift + bits)) == prefix >> (shift + bits));
-                    const unsigned bin = v[u] >> shift & ((1u << bits) - 1);
-                    // many equal scores would queue at one counter: a warp that agrees counts once
-                    int same;
-                    __match_all_sync(kFull, in ? bin : 0xffffffffu, &same);
-                    if (same) {
-                        if (in && lane == 0) atomicAdd(hist + bin, 32u);
-                    } else if (in) {
-                        atomicAdd(hist + bin, 1u);
-                    }
-                }
+            for (int u = 0; u < kAhead; ++u) {
+                const long long row = __shfl_sync(kFull, rows, (j + u) & 31);
+                ok[u] = j + u < m && inside((base + j + u) * 32 + lane);
+                x[u] = ok[u] && row >= 0 ? load(scores + row + lane) : __uint_as_float(0x7fc00000);  // a NaN
             }
-            __syncthreads();
-            // counts from the top: thread t holds bins 2047 - 2t and 2046 - 2t
-            const unsigned h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
-            unsigned s = h0 + h1;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned t = __shfl_up_sync(kFull, s, o);
-                if (lane >= o) s += t;
+            for (int u = 0; u < kAhead; ++u) {
+                if (j + u >= m) break;
+                const unsigned v = ordered(x[u]);
+                const int i = (base + j + u) * 32 + lane;
+                if (i < kCached) cache[i] = v;
+                count(ok[u], v >> 21);
             }
-            if (lane == 31) warp_sum_[warp] = s;
-            __syncthreads();
-            unsigned before = s - h0 - h1;
-            for (int i = 0; i < warp; ++i) before += warp_sum_[i];
-            if (before < left && left <= before + h0 + h1) {  // one thread's
-                const bool second = left > before + h0;
-                found[0] = unsigned(kBins - 1 - 2 * threadIdx.x) - (second ? 1u : 0u);
-                found[1] = left - before - (second ? h0 : 0u);
-            }
-            __syncthreads();
-            prefix |= found[0] << shift;
-            left = found[1];
         }
     }
-    // keys above `prefix` stay, and the first `left` of those equal to it
-    const int seg = (n + 32 * kSelWarps - 1) / (32 * kSelWarps) * 32, s0 = warp * seg, s1 = min(n, s0 + seg);
-    auto value = [&](int i) { return i < kCached ? cache[i] : fetch(i); };
-    int above = 0, equal = 0;
-    if (k > 0)
-        for (int i = s0; i < s1; i += 32) {
-            const unsigned v = i + lane < s1 ? value(i + lane) : 0u;
-            above += __popc(__ballot_sync(kFull, i + lane < s1 && v > prefix));
-            equal += __popc(__ballot_sync(kFull, i + lane < s1 && v == prefix));
+    find(21);
+    const unsigned top = prefix;
+    clear();
+    // the keys of the bin, listed; and counted by the next digit
+    for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
+        const unsigned v = value(i);
+        const bool in = inside(i) && (v & 0xffe00000u) == top;
+        const unsigned those = __ballot_sync(kFull, in);
+        if (!those) continue;
+        unsigned at = 0;
+        if (lane == 0) at = atomicAdd(&listed, unsigned(__popc(those)));
+        at = __shfl_sync(kFull, at, 0) + __popc(those & ((1u << lane) - 1));
+        if (in && at < kListed) list[at] = v;
+        count(in, v >> 10 & 2047);
+    }
+    find(10);
+    const bool all_listed = listed <= kListed;
+    const int in_list = int(min(listed, unsigned(kListed)));
+    __syncthreads();
+    clear();
+    if (all_listed) {
+        for (int i = threadIdx.x; i < in_list; i += kSelThreads)
+            if ((list[i] & 0xfffffc00u) == prefix) atomicAdd(hist + (list[i] & 1023), 1u);
+    } else {
+        for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
+            const unsigned v = value(i);
+            count(inside(i) && (v & 0xfffffc00u) == prefix, v & 1023);
         }
+    }
+    find(0);
+    // keys above `prefix` stay, and the first `left` of those equal to it
+    int above = 0, equal = 0;
+    for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
+        const unsigned v = value(i);
+        const bool in = inside(i);
+        above += in && v > prefix;
+        equal += in && v == prefix;
+    }
+    above = __reduce_add_sync(kFull, above);
+    equal = __reduce_add_sync(kFull, equal);
     if (lane == 0) {
         warp_n[0][warp] = above;
         warp_n[1][warp] = equal;
     }
     __syncthreads();
-    int at = 0, ties = 0;  // of the stretches before
-    for (int i = 0; i < warp; ++i) {
-        at += warp_n[0][i];
-        ties += warp_n[1][i];
-    }
+    const bool before = lane < warp;  // of the stretches before
+    int at = __reduce_add_sync(kFull, before ? warp_n[0][lane] : 0), ties = __reduce_add_sync(kFull, before ? warp_n[1][lane] : 0);
     at += min(ties, int(left));
-    for (int i = threadIdx.x; i < lo; i += kSelThreads) kept[i] = i;
-    for (int i = threadIdx.x; i < L - hi; i += kSelThreads) kept[lo + k + i] = hi + i;
-    if (k == 0) return;
     const unsigned below = (1u << lane) - 1;
-    for (int i = s0; i < s1; i += 32) {
-        const bool in = i + lane < s1;
-        const unsigned v = in ? value(i + lane) : 0u;
+    for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
+        const bool in = inside(i);
+        const unsigned v = value(i);
         const unsigned eq = __ballot_sync(kFull, in && v == prefix);
         const bool stays = in && (v > prefix || (v == prefix && ties + __popc(eq & below) < int(left)));
         const unsigned st = __ballot_sync(kFull, stays);
-        if (stays) kept[lo + at + __popc(st & below)] = lo + i + lane;
+        if (stays) kept[lo + at + __popc(st & below)] = first * 32 + i;
         at += __popc(st);
         ties += __popc(eq);
     }
@@ -220,8 +276,8 @@ cudaError_t launch_evict(const EvictParams &e, int dtype, cudaStream_t stream) {
     const Params &p = e.p;
     const bool paged = p.page_table != nullptr;
     const dim3 heads(unsigned(p.Hkv), unsigned(p.B));
-    const int middle = p.max_len < kCached ? p.max_len : kCached;
-    const size_t smem = kSelSmem - size_t(kCached - middle) * 4;
+    const int most_cached = (p.max_len + 31) / 32 * 32;  // of whole blocks
+    const size_t smem = kSelSmem - (most_cached < kCached ? size_t(kCached - most_cached) * 4 : 0);
     auto select = [&](auto kern) {
         const cudaError_t r = ensure_smem(kern, kSelSmem);
         return r != cudaSuccess ? r : launch_kernel(kern, heads, dim3(kSelThreads), smem, stream, true, 0, false, e);

@@ -97,9 +97,9 @@ struct WeightParams {
     const float *scores;
     float *scores_out;
     float decay;
-    int fresh, splits;
+    int fresh;
 };
-cudaError_t launch_key_weights(WeightParams w, cudaStream_t stream);
+cudaError_t launch_key_weights(const WeightParams &w, cudaStream_t stream);
 
 struct EvictParams {
     Params p;                  // shapes, k, v, the cache's addressing

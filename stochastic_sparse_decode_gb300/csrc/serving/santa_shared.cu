@@ -19,9 +19,9 @@
 // forms weights.  They take two tiles of 128 rows over the same blocks or, with at most 128 rows,
 // the even and the odd blocks of one tile.
 //
-// Tensor memory of a stream, 256 columns: O in 0 .. D - 1, S in 128 .. 191, the parts of E in
-// 192 .. 223, 224 .. 255 and, the smallest, 128 .. 159, over S, whose 16 columns have been read
-// when 8 columns of it are written.
+// Tensor memory of a stream, 256 columns: O in 0 .. D - 1, S in 128 .. 191, the larger parts of E in
+// 192 .. 223 and 224 .. 255; the smallest part has no room there and lies in shared memory.  So S of
+// the next block can be formed as soon as E of this one is, before or beside E V.
 //
 // fp32 (shared_f32_kernel): 64 rows x 32 keys from shared memory on the FMA pipe.
 #include "santa_split.cuh"
@@ -35,37 +35,51 @@ namespace {
 constexpr int kRows = 128;     // rows of a stream's tile
 constexpr int kKeys = 64;      // keys of a block
 constexpr int kHalf = 32;      // keys of a TMA box
-constexpr int kThreads = 320;  // streams 0 and 1 (four warps each), producer, products
+constexpr int kThreads = 384;  // streams 0 and 1 (four warps each); a producer, two warps of products, an idle one
+// Registers per thread: launched with 168 (the file of 65536 over 384 threads), of which the last
+// warpgroup gives back what the streams, with D sums and a block's values per thread, take.
+constexpr int kLaunchRegs = 168, kStreamRegs = 224, kOtherRegs = 56;
+static_assert(2 * kStreamRegs + kOtherRegs <= 3 * kLaunchRegs, "a larger share would wait forever");
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 template <int D>
 struct MmaGeom {
     static constexpr int kBoxes = D / 64;                   // 128-byte columns of a row
     static constexpr int kTile = kKeys * D * 2;             // K or V of a block
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr size_t kQ = 0;                         // [2] tiles of Q
-    static constexpr size_t kStage0 = size_t(2) * kRows * D * 2;
+    static constexpr size_t kLow = size_t(2) * kRows * D * 2;      // [2] tiles of E's smallest part
+    static constexpr size_t kStage0 = kLow + size_t(2) * kRows * kKeys * 2;
     static constexpr size_t kBars = kStage0 + size_t(kStages) * 2 * kTile;
-    static constexpr size_t kTotal = kBars + (2 * kStages + 9) * 8 + kStages * 8 + 16;
+    static constexpr size_t kTotal = kBars + (2 * kStages + 13) * 8 + kStages * 8 + 16;
     static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
-// The segments of a CTA's stretch: blocks blk .. blk + n - 1 of an item.
+// The segments of a CTA's stretch: blocks blk .. blk + n - 1 of an item.  (Units are counted in
+// 31 bits.)
 struct Segments {
-    long long u, end;
+    int u, end;
     int item, blk, n, rows, first;  // rows of the item, from row `first` of the KV head on
     bool both;                      // the streams share the item's blocks
     __device__ __forceinline__ explicit Segments(const SharedParams &sp) {
-        const long long X = (long long)sp.p.Hkv * sp.tiles * sp.nb;
-        u = stretch_start(X, sp.ctas, blockIdx.x);
-        end = stretch_start(X, sp.ctas, blockIdx.x + 1);
+        const int X = sp.p.Hkv * sp.tiles * sp.nb, q = X / sp.ctas, r = X - q * sp.ctas, c = blockIdx.x;
+        u = q * c + min(c, r);  // as stretch_start
+        end = u + q + (c < r ? 1 : 0);
         n = 0;
     }
     __device__ __forceinline__ bool next(const SharedParams &sp, int tile_rows, int streams) {
         u += n;
         if (u >= end) return false;
-        item = int(divide(u, sp.nb));
-        blk = int(u - (long long)item * sp.nb);
-        n = int(min((long long)(sp.nb - blk), end - u));
+        item = u / sp.nb;
+        blk = u - item * sp.nb;
+        n = min(sp.nb - blk, end - u);
         first = item % sp.tiles * tile_rows * streams;
         rows = min(sp.rows - first, tile_rows * streams);
         both = streams == 2 && rows <= tile_rows;
@@ -76,6 +90,59 @@ struct Segments {
     __device__ __forceinline__ int place(int t, int i) const { return both ? 2 * i + t : i; }
 };
 
+// Logits of keys that do not count become -inf (their weight 0), whatever they hold.
+__device__ __forceinline__ void drop(float (&x)[16], uint32_t seen) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (!(seen >> j & 1)) x[j] = -INFINITY;
+}
+// A row's weights of 32 keys (x, y: their raw logits), as the parts of E: two in tensor memory from
+// columns hi_at and mid_at on, the smallest at `low` (the row's 128 bytes in the swizzle of the operand),
+// pieces of 16 bytes from `piece` on.  Adds them to sum.
+__device__ __forceinline__ void half_weights(float (&x)[16], float (&y)[16], float scale2, float ref, uint32_t hi_at,
+                                             uint32_t mid_at, unsigned char *low, int piece, int r, float2 &sum) {
+    const float2 scale = make_float2(scale2, scale2), shift = make_float2(-ref, -ref);
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float2 e = __ffma2_rn(d ? make_float2(y[2 * j], y[2 * j + 1]) : make_float2(x[2 * j], x[2 * j + 1]), scale, shift);
+            e = make_float2(ex2(e.x), ex2(e.y));
+            sum = __fadd2_rn(sum, e);
+            // what a part leaves over is exact
+            uint32_t u = __float_as_uint(e.x), v = __float_as_uint(e.y);
+            hi[j] = __byte_perm(u, v, 0x7632);
+            e = __fadd2_rn(e, make_float2(-__uint_as_float(u & 0xffff0000u), -__uint_as_float(v & 0xffff0000u)));
+            u = __float_as_uint(e.x), v = __float_as_uint(e.y);
+            mid[j] = __byte_perm(u, v, 0x7632);
+            e = __fadd2_rn(e, make_float2(-__uint_as_float(u & 0xffff0000u), -__uint_as_float(v & 0xffff0000u)));
+            lo[j] = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);
+        }
+        tmem_store8(hi_at + 8 * d, hi);
+        tmem_store8(mid_at + 8 * d, mid);
+        *reinterpret_cast<uint4 *>(low + (((piece + 2 * d) ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4 *>(low + (((piece + 2 * d + 1) ^ (r & 7)) << 4)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    }
+}
+// O = O * sc + the block's sums.
+template <int D>
+__device__ __forceinline__ void add_sums(uint32_t base, float2 (&O)[D / 2], float sc) {
+    const float2 sc2 = make_float2(sc, sc);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        float x[16], y[16];
+        tmem_load16(base + 32 * c, x);
+        tmem_load16(base + 32 * c + 16, y);
+        tmem_wait(x, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            O[16 * c + j] = __ffma2_rn(O[16 * c + j], sc2, make_float2(x[2 * j], x[2 * j + 1]));
+            O[16 * c + 8 + j] = __ffma2_rn(O[16 * c + 8 + j], sc2, make_float2(y[2 * j], y[2 * j + 1]));
+        }
+    }
+}
+
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -83,12 +150,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     using Geo = MmaGeom<D>;
     constexpr int NS = Geo::kStages;
     const Params &p = sp.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // uniform
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Geo::kBars), *empty = full + NS;
-    // per stream: S is there; E is there; O is there; Q is there
-    uint64_t *sready = empty + NS, *eready = sready + 2, *oready = eready + 2, *qready = oready + 2, *fin = qready + 2;
-    uint2 *valid = reinterpret_cast<uint2 *>(fin + 1);  // a stage's keys that count, a bit each
+    // per stream: S is there; E is there, half by half; O is there; Q is there; all products have ended
+    uint64_t *sready = empty + NS, *eready = sready + 2, *oready = eready + 4, *qready = oready + 2, *fin = qready + 2;
+    uint64_t *go = fin + 2;  // stream 0 has its first weights
+    uint2 *valid = reinterpret_cast<uint2 *>(go + 1);  // a stage's keys that count, a bit each
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(valid + NS);
 
     if (threadIdx.x == 0) {
@@ -98,11 +166,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sready[t], 1);
-            mbar_init(&eready[t], kRows);
+            mbar_init(&eready[2 * t], kRows);
+            mbar_init(&eready[2 * t + 1], kRows);
             mbar_init(&oready[t], 1);
             mbar_init(&qready[t], kRows);
+            mbar_init(&fin[t], 1);
         }
-        mbar_init(fin, 1);
+        mbar_init(go, 1);
         fence_barrier_init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -111,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = __shfl_sync(kFull, *tmem_at, 0);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -119,7 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segments sg(sp);
     int it = 0;  // blocks of the CTA before this segment
 
-    if (warp == 8) {  // producer
+    if (warp >= 8) fewer_registers<kOtherRegs>();
+    if (warp == 11) {
+    } else if (warp == 8) {  // producer
         bool ok = true;
         while (ok && sg.next(sp, kRows, 2)) {
             const int kvh = sg.item / sp.tiles;
@@ -172,69 +244,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (!mbar_try_wait(&full[i % NS], (i / NS) & 1) && clock64() - t0 < kWaitCycles) {
                 }
         }
-    } else if (warp == 9) {  // products
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t phQ[2] = {0, 0}, phE[2] = {0, 0}, phO[2] = {0, 0};
-            constexpr uint32_t kind_s = mma_kind(kRows, kKeys, false), kind_o = mma_kind(kRows, D, true);
-            const uint32_t q0 = smem_addr(smem + Geo::kQ), st0 = smem_addr(smem + Geo::kStage0);
-            // S of stream t's i-th block
-            auto scores = [&](int t, int i) {
-                const int b = it + sg.place(t, i), s = b % NS;
-                if (!mbar_wait(&full[s], (b / NS) & 1)) return false;
-                tc_after_sync();
-                const uint32_t q = q0 + t * kRows * D * 2, k = st0 + s * 2 * Geo::kTile;
+    } else if (warp >= 9) {  // products of stream t: the warp as one, an elected lane issues
+        const int t = warp - 9;
+        bool ok = true;
+        bool gone = false;
+        uint32_t phQ = 0, ph = 0;
+        constexpr uint32_t kind_s = mma_kind(kRows, kKeys, false), kind_o = mma_kind(kRows, D, true);
+        const uint32_t base = tmem + t * 256;
+        const uint64_t q = operand(smem_addr(smem + Geo::kQ) + t * kRows * D * 2, 16, 1024);
+        const uint64_t k0 = operand(smem_addr(smem + Geo::kStage0), 16, 1024);
+        const uint64_t v0 = operand(smem_addr(smem + Geo::kStage0) + Geo::kTile, kKeys * 128, 1024);
+        const uint64_t low = operand(smem_addr(smem + Geo::kLow) + t * kRows * kKeys * 2, 16, 1024);
+        auto wait = [&](uint64_t *bar, uint32_t phase) { return bool(__all_sync(kFull, mbar_wait(bar, phase))); };
+        // S of the stream's i-th block, whose K is there
+        auto scores = [&](int i) {
+            const int s = (it + sg.place(t, i)) % NS;
+            const uint64_t k = k0 + __shfl_sync(kFull, s * (2 * Geo::kTile / 16), 0);
+            if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    mma_ss(tmem + t * 256 + 128, operand(q + (ks >> 2) * kRows * 128 + (ks & 3) * 32, 16, 1024),
-                           operand(k + (ks >> 2) * kKeys * 128 + (ks & 3) * 32, 16, 1024), kind_s, ks > 0);
+                    mma_ss(base + 128, q + ((ks >> 2) * kRows * 128 + (ks & 3) * 32) / 16,
+                           k + ((ks >> 2) * kKeys * 128 + (ks & 3) * 32) / 16, kind_s, ks > 0);
                 mma_commit(&sready[t]);
-                return true;
-            };
-            // O of the same
-            auto sums = [&](int t, int i) {
-                if (!mbar_wait(&eready[t], phE[t])) return false;
-                phE[t] ^= 1;
-                tc_after_sync();
-                const int s = (it + sg.place(t, i)) % NS;
-                const uint32_t v = st0 + s * 2 * Geo::kTile + Geo::kTile, base = tmem + t * 256;
+            }
+            __syncwarp();
+        };
+        auto arrived = [&](int i, bool now) {  // K and V of the i-th block; `now`: without waiting
+            const int block = it + sg.place(t, i);
+            const bool there = now ? bool(__all_sync(kFull, mbar_try_wait(&full[block % NS], (block / NS) & 1)))
+                                   : wait(&full[block % NS], (block / NS) & 1);
+            tc_after_sync();
+            return there;
+        };
+        // O of half h of the i-th block
+        auto sums = [&](int i, int h) {
+            const int s = (it + sg.place(t, i)) % NS;
+            const uint64_t v = v0 + __shfl_sync(kFull, s * (2 * Geo::kTile / 16), 0);
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < 3; ++part)  // the smallest first
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                        mma_ts(base, base + (part == 0 ? 128 : part == 1 ? 224 : 192) + ks * 8,
-                               operand(v + ks * 16 * 128, kKeys * 128, 1024), kind_o, part + ks > 0);
-                mma_commit(&oready[t]);
-                mma_commit(&empty[s]);
-                if (sg.both) mbar_arrive(&empty[s]);
-                return true;
-            };
-            while (ok && sg.next(sp, kRows, 2)) {
-                const int n0 = sg.count(0), n1 = sg.count(1);
-                for (int t = 0; ok && t < 2; ++t) {
-                    if ((t ? n1 : n0) == 0) continue;
-                    ok = mbar_wait(&qready[t], phQ[t]) && scores(t, 0);
-                    phQ[t] ^= 1;
-                }
-                for (int i = 0; ok && i < n0; ++i)
-                    for (int t = 0; ok && t < 2; ++t) {
-                        const int n = t ? n1 : n0;
-                        if (i >= n) continue;
-                        ok = sums(t, i);
-                        if (!ok) break;
-                        if (i + 1 < n) {  // S takes the place of E
-                            ok = mbar_wait(&oready[t], phO[t]) && scores(t, i + 1);
-                        }
-                        phO[t] ^= 1;
+                    for (int k2 = 0; k2 < kHalf / 16; ++k2) {
+                        const int ks = h * (kHalf / 16) + k2;
+                        if (part == 0)
+                            mma_ss(base, low + ks * 32 / 16, v + ks * 16 * 128 / 16, kind_o, h + k2 > 0);
+                        else
+                            mma_ts(base, base + (part == 1 ? 224 : 192) + ks * 8, v + ks * 16 * 128 / 16, kind_o, true);
                     }
-                it += sg.n;
+                if (h == 1) {
+                    mma_commit(&oready[t]);
+                    mma_commit(&empty[s]);
+                    if (sg.both) mbar_arrive(&empty[s]);
+                }
             }
-            if (!ok) give_up();
-            mma_commit(fin);  // every product has ended before tensor memory is given back
-            if (!mbar_wait(fin, 0)) give_up();
+            __syncwarp();
+        };
+        while (ok && sg.next(sp, kRows, 2)) {
+            const int n = sg.count(t);
+            if (n > 0) {
+                ok = wait(&qready[t], phQ) && arrived(0, false);
+                phQ ^= 1;
+                // stream 1 begins half a block later: in step, each would wait for the pipe that the other uses
+                if (ok && t == 1 && !gone) ok = wait(go, 0);
+                gone = gone || t == 1;
+                if (ok) scores(0);
+            }
+#pragma unroll 1
+            for (int i = 0; ok && i < n; ++i) {
+                ok = wait(&eready[2 * t], ph);
+                if (!ok) break;
+                tc_after_sync();
+                sums(i, 0);
+                if (t == 0 && !gone) {
+                    if (elect_one()) mbar_arrive(go);
+                    gone = true;
+                    __syncwarp();
+                }
+                ok = wait(&eready[2 * t + 1], ph);
+                ph ^= 1;
+                if (!ok) break;
+                tc_after_sync();
+                // the next S first, unless its K is late
+                const bool next = i + 1 < n, early = next && arrived(i + 1, true);
+                if (early) scores(i + 1);
+                sums(i, 1);
+                if (next && !early) {
+                    ok = arrived(i + 1, false);
+                    if (ok) scores(i + 1);
+                }
+            }
+            it += sg.n;
         }
+        if (!ok && lane == 0) give_up();
+        __syncwarp();
+        if (elect_one()) mma_commit(&fin[t]);  // every product has ended before tensor memory is given back
+        __syncwarp();
+        if (!wait(&fin[t], 0) && lane == 0) give_up();
         __syncwarp();
     } else {  // weights
+        more_registers<kStreamRegs>();
         const int t = warp >> 2, r = threadIdx.x & (kRows - 1);
         const uint32_t base = tmem + t * 256 + (uint32_t(warp & 3) << 21);
         const float scale2 = p.scale * 1.4426950408889634f;  // logits in base 2
@@ -244,17 +352,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int kvh = sg.item / sp.tiles, row0 = sg.first + (sg.both ? 0 : t * kRows);
             const int rows = sg.both ? sg.rows : min(kRows, sg.rows - t * kRows);  // may be <= 0
             const int n = sg.count(t);
-            // the stream's tile of Q, rows of zeros behind the last
-            for (int i = r; i < kRows * D / 8 && n > 0; i += kRows) {
-                const int qr = i / (D / 8), vec = i % (D / 8);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (qr < rows) {
+            // the stream's tile of Q, rows of zeros behind the last: a piece of 16 bytes per thread and round
+            if (n > 0) {
+                constexpr int kVecs = D / 8, kRounds = kRows * kVecs / kRows;
+                const int vec = r % kVecs;
+                uint4 x[kRounds];
+#pragma unroll
+                for (int u = 0; u < kRounds; ++u) {
+                    const int qr = r / kVecs + u * (kRows / kVecs);
                     const int b = (row0 + qr) / p.G, g = (row0 + qr) - b * p.G;
-                    x = load(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                             (size_t(b) * p.Hq + kvh * p.G + g) * D) + vec);
+                    x[u] = qr < rows ? load(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                                            (size_t(b) * p.Hq + kvh * p.G + g) * D) + vec)
+                                     : make_uint4(0, 0, 0, 0);
                 }
-                *reinterpret_cast<uint4 *>(smem + Geo::kQ + size_t(t) * kRows * D * 2 + (vec >> 3) * kRows * 128 + qr * 128 +
-                                           (((vec & 7) ^ (qr & 7)) << 4)) = x;
+#pragma unroll
+                for (int u = 0; u < kRounds; ++u) {
+                    const int qr = r / kVecs + u * (kRows / kVecs);
+                    *reinterpret_cast<uint4 *>(smem + Geo::kQ + size_t(t) * kRows * D * 2 + (vec >> 3) * kRows * 128 +
+                                               qr * 128 + (((vec & 7) ^ (qr & 7)) << 4)) = x[u];
+                }
             }
             if (n > 0) {  // (a stream that has no block must not run ahead of its barrier's phase)
                 fence_proxy_async_smem();
@@ -262,108 +378,104 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&qready[t]);
             }
 
-            float O[D], M = -INFINITY, Z = 0.f;
+            float2 O[D / 2];
+            float M = -INFINITY, Z = 0.f;
 #pragma unroll
-            for (int i = 0; i < D; ++i) O[i] = 0.f;
+            for (int i = 0; i < D / 2; ++i) O[i] = make_float2(0.f, 0.f);
+            float sc = 0.f;  // of the block before
             for (int i = 0; i < n; ++i) {
                 const int b = it + sg.place(t, i), s = b % NS;
                 // the stage stays until this block's sums are formed, so its barrier's phase does too
-                ok = mbar_wait(&sready[t], ph) && mbar_wait(&full[s], (b / NS) & 1);
+                ok = mbar_wait(&full[s], (b / NS) & 1);
+                if (!ok) break;
+                const uint2 seen2 = valid[s];
+                ok = mbar_wait(&sready[t], ph);
                 if (!ok) break;
                 tc_after_sync();
-                const uint2 seen2 = valid[s];
-                const uint64_t seen = uint64_t(seen2.y) << 32 | seen2.x;
                 const bool whole = (seen2.x & seen2.y) == kFull;
-                float m = M;
-#pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    float x[16], y[16];
-                    tmem_load16(base + 128 + 32 * c, x);
-                    tmem_load16(base + 128 + 32 * c + 16, y);
-                    tmem_wait(x, y);
-                    if (!whole) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (!(seen >> (32 * c + j) & 1)) x[j] = -INFINITY;
-                            if (!(seen >> (32 * c + 16 + j) & 1)) y[j] = -INFINITY;
+                unsigned char *low = smem + Geo::kLow + size_t(t * kRows + r) * kKeys * 2;
+                float2 sum = make_float2(0.f, 0.f);
+                float ref, sc_next;
+                {
+                    float x[16], y[16];  // the first half
+                    {
+                        float u[16], v[16];
+                        tmem_load16(base + 160, u);
+                        tmem_load16(base + 176, v);
+                        tmem_load16(base + 128, x);
+                        tmem_load16(base + 144, y);
+                        tmem_wait(u, v);
+                        tmem_arrived(x, y);
+                        if (!whole) {
+                            drop(x, seen2.x);
+                            drop(y, seen2.x >> 16);
+                            drop(u, seen2.y);
+                            drop(v, seen2.y >> 16);
                         }
-                    }
+                        float m = M;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) m = fmaxf(m, fmaxf(x[j], y[j]));
+                        for (int j = 0; j < 16; ++j) m = fmaxf(fmaxf(m, fmaxf(x[j], y[j])), fmaxf(u[j], v[j]));
+                        ref = m == -INFINITY ? 0.f : m * scale2;
+                        sc_next = ex2(fmaf(M, scale2, -ref));
+                        M = m;
+                    }
+                    // (E of the block before has been read where S of this one is there: its products came first)
+                    half_weights(x, y, scale2, ref, base + 192, base + 224, low, 0, r, sum);
                 }
-                const float ref = m == -INFINITY ? 0.f : m * scale2;
-                const float sc = ex2(fmaf(M, scale2, -ref));
-                M = m;
-                float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-                for (int c = 0; c < kKeys / 16; ++c) {
-                    float x[16];
-                    tmem_load16(base + 128 + 16 * c, x);
-                    tmem_wait(x, x);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        x[j] = ex2(fmaf(x[j], scale2, -ref));
-                        if (!whole && !(seen >> (16 * c + j) & 1)) x[j] = 0.f;
-                    }
-                    uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float u = x[2 * j], v = x[2 * j + 1];
-                        z0 += u;
-                        z1 += v;
-                        // what a part leaves over is exact
-                        hi[j] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-                        u -= __uint_as_float(__float_as_uint(u) & 0xffff0000u);
-                        v -= __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-                        mid[j] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-                        u -= __uint_as_float(__float_as_uint(u) & 0xffff0000u);
-                        v -= __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-                        lo[j] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-                    }
-                    tmem_store8(base + 128 + 8 * c, lo);
-                    tmem_store8(base + 192 + 8 * c, hi);
-                    tmem_store8(base + 224 + 8 * c, mid);
+                if (i > 0) {
+                    ok = mbar_wait(&oready[t], ph ^ 1);
+                    if (!ok) break;
+                    tc_after_sync();
+                    add_sums<D>(base, O, sc);
                 }
-                Z = fmaf(Z, sc, z0 + z1);
+                sc = sc_next;
                 if (!whole) {  // weight 0 times a row that holds anything
                     unsigned char *v = smem + Geo::kStage0 + size_t(s) * 2 * Geo::kTile + Geo::kTile;
                     for (int j = r; j < kKeys * Geo::kBoxes * 8; j += kRows) {
                         const int key = (j >> 3) % kKeys, bx = (j >> 3) / kKeys;
-                        if (!(seen >> key & 1))
+                        if (!((key < 32 ? seen2.x : seen2.y) >> (key & 31) & 1))
                             *reinterpret_cast<uint4 *>(v + bx * kKeys * 128 + key * 128 + (j & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                     }
-                    fence_proxy_async_smem();
                 }
+                fence_proxy_async_smem();
                 tmem_wait_store();
                 tc_before_sync();
-                mbar_arrive(&eready[t]);
-                ok = mbar_wait(&oready[t], ph);
-                ph ^= 1;
-                if (!ok) break;
-                tc_after_sync();
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
+                mbar_arrive(&eready[2 * t]);
+                {
                     float x[16], y[16];
-                    tmem_load16(base + 32 * c, x);
-                    tmem_load16(base + 32 * c + 16, y);
+                    tmem_load16(base + 160, x);
+                    tmem_load16(base + 176, y);
                     tmem_wait(x, y);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        O[32 * c + j] = fmaf(O[32 * c + j], sc, x[j]);
-                        O[32 * c + 16 + j] = fmaf(O[32 * c + 16 + j], sc, y[j]);
+                    if (!whole) {
+                        drop(x, seen2.y);
+                        drop(y, seen2.y >> 16);
                     }
+                    half_weights(x, y, scale2, ref, base + 208, base + 240, low, 4, r, sum);
                 }
+                Z = fmaf(Z, sc, sum.x + sum.y);
+                fence_proxy_async_smem();
+                tmem_wait_store();
+                tc_before_sync();
+                mbar_arrive(&eready[2 * t + 1]);
+                ph ^= 1;
+            }
+            if (ok && n > 0) {
+                ok = mbar_wait(&oready[t], ph ^ 1);
+                tc_after_sync();
+                if (ok) add_sums<D>(base, O, sc);
             }
             if (!ok) break;
             if (r < rows) {
                 const size_t at = (size_t(sg.item + blockIdx.x) * 2 + t) * kRows + r;
                 sp.mz[at] = make_float2(M == -INFINITY ? M : M * scale2, Z);
-                float4 *o = reinterpret_cast<float4 *>(sp.o + at * D);
-                if (n > 0)
+                if (n > 0)  // whole sectors of 32 bytes per thread
 #pragma unroll
-                    for (int i = 0; i < D / 4; ++i)
-                        o[i] = make_float4(O[4 * i], O[4 * i + 1], O[4 * i + 2], O[4 * i + 3]);
+                    for (int i = 0; i < D / 8; ++i)
+                        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(sp.o + at * D + 8 * i),
+                                     "f"(O[4 * i].x), "f"(O[4 * i].y), "f"(O[4 * i + 1].x), "f"(O[4 * i + 1].y),
+                                     "f"(O[4 * i + 2].x), "f"(O[4 * i + 2].y), "f"(O[4 * i + 3].x), "f"(O[4 * i + 3].y)
+                                     : "memory");
             }
             it += sg.n;
         }
@@ -627,7 +739,14 @@ cudaError_t launch_mma(const SharedParams &sp, cudaStream_t stream) {
             return cudaErrorUnknown;
     }
     auto go = [&](auto kern) {
-        const cudaError_t r = ensure_smem(kern, MmaGeom<D>::kTotal);
+        cudaError_t r = ensure_smem(kern, MmaGeom<D>::kTotal);
+        static bool checked = false;  // the streams' registers come out of those the kernel is launched with
+        if (r == cudaSuccess && !checked) {
+            cudaFuncAttributes a;
+            r = cudaFuncGetAttributes(&a, kern);
+            if (r == cudaSuccess && a.numRegs < kLaunchRegs) r = cudaErrorNotSupported;
+            checked = r == cudaSuccess;
+        }
         if (r != cudaSuccess) return r;
         return launch_kernel(kern, dim3(unsigned(sp.ctas)), dim3(kThreads), MmaGeom<D>::kTotal, stream, true, 0, false,
                              maps[0], maps[1], sp);
@@ -656,6 +775,7 @@ cudaError_t launch_shared(SharedParams &sp, int dtype, cudaStream_t stream, cons
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const long long X = (long long)sp.p.Hkv * sp.tiles * sp.nb, most = (X + kMinBlocks - 1) / kMinBlocks;
+    if (X > 0x7fffffffLL) return cudaErrorNotSupported;
     const int ctas = sms < kSplitCtaBound ? sms : kSplitCtaBound;
     sp.ctas = most < ctas ? int(most) : ctas;
     record_event(tm.begin, stream);

@@ -9,13 +9,24 @@ namespace santa {
 // Shared-memory operand of 16-bit elements in the 128-byte swizzle that TMA writes: groups of
 // 8 rows x 128 bytes (1024 bytes, 1024-byte aligned) `group_bytes` apart along the rows, blocks
 // of 128 bytes of a row `block_bytes` apart (used where the row is the non-contracted dimension).
+// (The address below 256 KB, so its 14 bits need no mask, and a step along the operand is an
+// addition of step >> 4.)
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t block_bytes, uint32_t group_bytes) {
-    return uint64_t((addr >> 4) & 0x3fff) | uint64_t((block_bytes >> 4) & 0x3fff) << 16 |
-           uint64_t((group_bytes >> 4) & 0x3fff) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+    const uint32_t low = (addr >> 4) + ((block_bytes >> 4) << 16);
+    const uint32_t high = group_bytes >> 4 | 1u << 14 | 2u << 29;
+    return uint64_t(high) << 32 | low;
 }
 // bf16 x bf16 -> fp32, M x N; b_rows: B's rows are the contracted dimension.
 constexpr uint32_t mma_kind(int M, int N, bool b_rows) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_rows ? 1u << 16 : 0u) | uint32_t(N >> 3) << 17 | uint32_t(M >> 4) << 24;
+}
+// One lane of a converged warp, the same each time.  Products are issued by warps that run as one up to
+// this choice: their operands are then uniform (in a lane's own branch every product took 110 cycles to
+// issue, against 32 to 64 that it takes the tensor cores).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 // D (tensor memory) = A B, or += with `add`; 16 elements of the contracted dimension.  One thread.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
@@ -59,17 +70,18 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&x)[16]) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait(float (&x)[16], float (&y)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
+// (No instruction: ties the values of other loads that a tmem_wait has waited for to the place behind it.)
+__device__ __forceinline__ void tmem_arrived(float (&x)[16], float (&y)[16]) {
+    asm volatile(""
                  : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
-                   "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15])
-                 :
-                 : "memory");
+                   "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]));
     asm volatile(""
                  : "+f"(y[0]), "+f"(y[1]), "+f"(y[2]), "+f"(y[3]), "+f"(y[4]), "+f"(y[5]), "+f"(y[6]), "+f"(y[7]),
-                   "+f"(y[8]), "+f"(y[9]), "+f"(y[10]), "+f"(y[11]), "+f"(y[12]), "+f"(y[13]), "+f"(y[14]), "+f"(y[15])
-                 :
-                 : "memory");
+                   "+f"(y[8]), "+f"(y[9]), "+f"(y[10]), "+f"(y[11]), "+f"(y[12]), "+f"(y[13]), "+f"(y[14]), "+f"(y[15]));
+}
+__device__ __forceinline__ void tmem_wait(float (&x)[16], float (&y)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    tmem_arrived(x, y);
 }
 // 8 columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8]) {
