@@ -197,9 +197,13 @@ class Decoder:
                              "not on the current CUDA device")
         return _raw_stream(dev) if stream is None else _stream(stream)
 
+    def _new(self, shape, dtype, dev):
+        self._stream(dev, None)  # refuses a device that is not the current one
+        return torch.empty(shape, dtype=dtype, device=dev)
+
     def _out(self, out, dev):
         if out is None:
-            return torch.empty(self._q_shape, dtype=torch.float32, device=dev)
+            return self._new(self._q_shape, torch.float32, dev)
         if not _fits(out, _F32, self._q_shape, dev):
             self._refuse("out", out, _F32, self._q_shape, dev)
         return out
@@ -354,7 +358,7 @@ class Decoder:
                 self._refuse("k", k, self._dt, self._kv_shape, dev)
         indptr, pref = self._where(kv_indptr, pages, dev)
         if out is None:
-            out = scores if scores is not None else torch.zeros((p.num_kv_heads, p.total_tokens), device=dev)
+            out = scores if scores is not None else self._new((p.num_kv_heads, p.total_tokens), torch.float32, dev).zero_()
         sp = None if scores is None else self._plane("scores", scores, p.total_tokens, dev)
         op = self._plane("out", out, p.total_tokens, dev)
         if not 0 <= fresh < 1 << 31:
@@ -417,11 +421,11 @@ class Decoder:
             pout = ctypes.byref(Pages(table_out.data_ptr(), None, size, table_out.shape[1], rows // size))
         shape = (p.batch, p.num_kv_heads, sinks + recent + budget)
         if kept is None:
-            kept = torch.empty(shape, dtype=torch.int32, device=dev)
+            kept = self._new(shape, torch.int32, dev)
         elif not _fits(kept, _I32, shape, dev):
             self._refuse("kept", kept, _I32, shape, dev)
         if lens_out is None:
-            lens_out = torch.empty(p.batch, dtype=torch.int32, device=dev)
+            lens_out = self._new((p.batch,), torch.int32, dev)
         elif not _fits(lens_out, _I32, (p.batch,), dev):
             self._refuse("lens_out", lens_out, _I32, (p.batch,), dev)
         _check("santa_evict", lib().santa_evict(
@@ -559,7 +563,7 @@ class Decoder:
             qp, qs = self._rows("q", q, n, p.num_q_heads, dev)
             shape = (n, p.num_q_heads, d)
             if out is None:
-                out = torch.empty(shape, dtype=q.dtype, device=dev)
+                out = self._new(shape, q.dtype, dev)
             elif not _fits(out, self._dt, shape, dev):
                 self._refuse("out", out, self._dt, shape, dev)
             op = out.data_ptr()
