@@ -102,7 +102,7 @@ Timing timing(const santa_debug *dbg) {
 }
 
 // The attention over a cache of k and v, or, with `four_bit`, over kv4.  The keys before `first`
-// do not count; own_mz (NULL: not wanted) receives each head's (M, Z).
+// do not count; own_mz (NULL: not wanted) receives each head's (M, Z): the call behind the prefix kernel.
 int attend(bool four_bit, const santa_problem *p, const santa_window *w, const santa_pages *pages, const void *q,
            const void *k, const void *v, const void *kv4, const long long *kv_indptr, float *out, void *workspace,
            size_t workspace_bytes, const santa_debug *dbg, santa_stream_t stream_, int first = 0,
@@ -137,6 +137,7 @@ int attend(bool four_bit, const santa_problem *p, const santa_window *w, const s
     sp.p.out = out;
     sp.first = first;
     sp.own_mz = own_mz;
+    sp.beside = own_mz != nullptr;
     sp.window = w && w->window > 0 && w->window < p->max_len ? w->window : p->max_len;
     sp.sinks = w ? w->sinks : 0;
     sp.narrow = p->batch <= 128 && double(p->batch) * p->num_kv_heads * (p->max_len / 32 + 2) < 2147483648.0;

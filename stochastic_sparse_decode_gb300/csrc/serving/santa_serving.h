@@ -59,6 +59,7 @@ struct SplitParams {
     int narrow;                // at most 128 sequences whose units of 32 keys number below 2^31
     int first;                 // the first key that counts (a prefix before it is another kernel's)
     float2 *own_mz;            // [B][Hq] the (M, Z) that out is divided by, or NULL
+    int beside;                // the kernel before is the same call's and runs beside this one (santa_window.cu)
     const unsigned char *kv4;  // 4-bit cache (k and v unused)
     unsigned int *cnt;         // [B][Hkv] CTAs that have stored a part of the head
     float2 *part_mz;           // [CTAs][2][G] (M, Z) of a CTA's first and last head, where others share it

@@ -95,12 +95,19 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
     }
     fence_barrier_init();
     __syncwarp();
-    pdl_wait();
+    // Behind the prefix kernel of the same call nothing that this kernel reads or writes is that
+    // kernel's, and what came before has ended when that kernel lets this one start: it runs beside
+    // it, on SMs that it leaves free, and only ends after it, so that the kernel behind this one
+    // finds the work of both.
+    if (!sp.beside) pdl_wait();
     pdl_launch_dependents();
 
     Walk w;
     const int any = plan_walk<NW, kPaged>(sp, sh, w);
-    if (any < 0) return;
+    if (any < 0) {
+        if (sp.beside) pdl_wait();
+        return;
+    }
 
     auto issue = [&](int which, int row, int kvh) {
         if (lane != 0) return;
@@ -404,6 +411,7 @@ __global__ void __launch_bounds__(WindowGeom<T, D, GT>::kWarps * 32, 1)
                             : const_cast<const float *>(first_piece) + size_t(slot >> 1) * GT * D;
         },
         room);
+    if (sp.beside) pdl_wait();
 }
 
 // Tensor map of a [rows][Hkv][d] cache: boxes of 128 bytes of one head's row x 32 rows.
