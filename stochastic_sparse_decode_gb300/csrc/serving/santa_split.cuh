@@ -254,6 +254,22 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                 }
             if (size == 0) return -1;
             cta0 = (unsigned(e) - size) * p.Hkv + (blockIdx.x - unsigned(b) * p.Hkv) * size;
+        } else if (sp.beside && heads > gridDim.x && unsigned(most) <= kJoinUnits) {  // whole heads, so many each
+            ctas = int(gridDim.x);
+            auto first_unit = [&](unsigned head) {
+                const unsigned s = head / p.Hkv;
+                unsigned u = X;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (s / 32 == k && 32 * k < p.B) {
+                        const unsigned n = unsigned(__shfl_sync(kFull, nb[k], s % 32));
+                        u = (unsigned(__shfl_sync(kFull, end[k], s % 32)) - n) * p.Hkv + (head - s * p.Hkv) * n;
+                    }
+                return s < unsigned(p.B) ? u : X;
+            };
+            cta0 = first_unit(heads / gridDim.x * blockIdx.x + min(blockIdx.x, heads % gridDim.x));
+            size = first_unit(heads / gridDim.x * (blockIdx.x + 1) + min(blockIdx.x + 1, heads % gridDim.x)) - cta0;
+            if (size == 0) return -1;
         } else {
             const unsigned parts = min(gridDim.x, (X + kMinUnitsPerCta - 1) / kMinUnitsPerCta);
             ctas = int(parts);
