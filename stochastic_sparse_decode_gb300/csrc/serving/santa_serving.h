@@ -60,6 +60,7 @@ struct SplitParams {
     int first;                 // the first key that counts (a prefix before it is another kernel's)
     float2 *own_mz;            // [B][Hq] the (M, Z) that out is divided by, or NULL
     int beside;                // the kernel before is the same call's and runs beside this one (santa_window.cu)
+    int no_join;               // the units' results stand alone: equal stretches, whatever the heads
     const unsigned char *kv4;  // 4-bit cache (k and v unused)
     unsigned int *cnt;         // [B][Hkv] CTAs that have stored a part of the head
     float2 *part_mz;           // [CTAs][2][G] (M, Z) of a CTA's first and last head, where others share it
@@ -101,6 +102,8 @@ struct WeightParams {
     int fresh;
 };
 cudaError_t launch_key_weights(const WeightParams &w, cudaStream_t stream);
+// Pass 1 of prop on bf16 keys, bit for bit, by equal shares of the blocks that the sequences hold.
+cudaError_t launch_key_logits(const SplitParams &sp, const CUtensorMap &kmap, cudaStream_t stream, const Timing &tm);
 
 struct EvictParams {
     Params p;                  // shapes, k, v, the cache's addressing

@@ -174,6 +174,7 @@ __device__ __forceinline__ unsigned seen_bits(const Walk &w) {
 // The row of a sequence without a key.
 __device__ __forceinline__ void zero_row(const SplitParams &sp, int b) {
     const Params &p = sp.p;
+    if (!p.out) return;
     if (sp.own_mz)
         for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) sp.own_mz[size_t(b) * p.Hq + i] = make_float2(-INFINITY, 0.f);
     float4 *o = reinterpret_cast<float4 *>(p.out + size_t(b) * p.Hq * p.D);
@@ -241,7 +242,8 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
         }
         const unsigned X = unsigned(sum) * p.Hkv, heads = unsigned(p.B) * p.Hkv;
         unsigned cta0 = 0, size = 0;  // the CTA's stretch
-        if (heads <= gridDim.x && __reduce_max_sync(kFull, unsigned(most)) <= kJoinUnits + X / gridDim.x) {  // a CTA per head
+        most = int(__reduce_max_sync(kFull, unsigned(most)));
+        if (!sp.no_join && heads <= gridDim.x && unsigned(most) <= kJoinUnits + X / gridDim.x) {  // a CTA per head
             ctas = int(heads);
             if (blockIdx.x >= heads) return -1;
             b = blockIdx.x / p.Hkv;
