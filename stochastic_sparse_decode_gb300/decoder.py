@@ -546,15 +546,16 @@ class Decoder:
             if not _fits(positions, _I32, (n,), dev):
                 self._refuse("positions", positions, _I32, (None,), dev)
         else:
-            rows = positions.shape[0]
-            if positions.dtype not in _I32 or positions.dim() != 2 or (n > 1 and positions.stride(1) != 1) or (
-                    rows > 1 and positions.stride(0) < n):
+            step = positions.stride()
+            if positions.dtype not in _I32 or len(step) != 2 or (n > 1 and step[1] != 1):
                 self._refuse("positions", positions, _I32, (None, None), dev)
-            axis = tuple(axis)
-            at = (axis, rows, positions.stride(0) if rows > 1 else n)
+            rows = positions.shape[0]
+            at = (tuple(axis), rows, step[0] if rows > 1 else n)
+            if at[2] < n:
+                self._refuse("positions", positions, _I32, (None, None), dev)
             axes = self._axes.get(at) or self._axes_of(*at)
-            if len(axis) * 2 != cos_sin.shape[-1]:
-                raise ValueError(f"axis: {len(axis)} pairs, cos_sin has {cos_sin.shape[-1] // 2}")
+            if len(at[0]) * 2 != cos_sin.shape[-1]:
+                raise ValueError(f"axis: {len(at[0])} pairs, cos_sin has {cos_sin.shape[-1] // 2}")
         if cos_sin.dim() != 2 or not _fits(cos_sin, _F32, cos_sin.shape, dev):
             self._refuse("cos_sin", cos_sin, _F32, (None, None), dev)
         qp = kp = vp = op = kc = vc = qw = kw = None
