@@ -10,7 +10,7 @@
 // beyond are read again), the list takes up to kListed of them.
 // Then every warp counts the keys of its stretch above the threshold and equal to it, one scan
 // over the warps places them, and the indices are written in order.
-// The move is a second kernel over all SMs: `rows` destination rows of all KV heads per CTA,
+// Few rows are moved by the same CTA, many by a second kernel over all SMs: `rows` destination rows of all KV heads per CTA,
 // whose sources and destinations are looked up once, then copied in 16-byte pieces.
 #include "santa_serving.h"
 
@@ -30,19 +30,15 @@ __device__ __forceinline__ unsigned ordered(float x) {
     return x != x ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The indices that (sequence b, KV head kvh) keeps, into e.kept; every thread of the CTA.
 template <bool kPaged>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams e) {
+__device__ __forceinline__ void select_keys(const EvictParams &e, int b, int kvh, int L, long long start,
+                                            unsigned char *smem) {
     const Params &p = e.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = blockIdx.x, b = blockIdx.y;
-    extern __shared__ __align__(16) unsigned char smem[];
     unsigned *hist = reinterpret_cast<unsigned *>(smem), *list = hist + kBins, *cache = list + kListed;
     __shared__ unsigned warp_sum_[kSelWarps], found[2], listed;
     __shared__ int warp_n[2][kSelWarps];
-    pdl_wait();
-    pdl_launch_dependents();
-    long long start;
-    const int L = seq_bounds<kPaged>(p, b, &start);
     const int lo = min(e.sinks, L), hi = max(lo, L - e.recent), n = hi - lo, k = min(e.budget, n);
     const int n_out = min(L, e.keep);
     if (kvh == 0 && threadIdx.x == 0) e.lens_out[b] = n_out;
@@ -59,25 +55,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     const float *scores = e.scores + size_t(kvh) * p.total_tokens;
     const int first = lo / 32, blocks = (hi + 31) / 32 - first, seg = (blocks + kSelWarps - 1) / kSelWarps;
     const int s0 = min(blocks, warp * seg), s1 = min(blocks, s0 + seg);
-    auto inside = [&](int i) {  // key i of the middle's blocks
-        const int key = first * 32 + i;
-        return key >= lo && key < hi;
-    };
     auto row_of = [&](int blk) {  // its first cache row, -1: a bad page (a block lies on one page)
-        return blk < s1 ? key_row<kPaged>(p, b, start, (first + blk) * 32) : -1LL;
-    };
-    auto value = [&](int i) {
-        if (i < kCached) return cache[i];
-        if (!inside(i)) return 0u;
-        const long long row = key_row<kPaged>(p, b, start, first * 32 + i);
-        return row < 0 ? 0u : ordered(load(scores + row));
+        return blk < s1 ? int(key_row<kPaged>(p, b, start, (first + blk) * 32)) : -1;
     };
     // counts one key of a bin; a warp that agrees (many equal scores) counts once
     auto count = [&](bool in, unsigned bin) {
-        int same;
-        __match_all_sync(kFull, in ? bin : 0xffffffffu, &same);
-        if (same) {
-            if (in && lane == 0) atomicAdd(hist + bin, 32u);
+        const unsigned first_bin = __shfl_sync(kFull, bin, 0);
+        if (__all_sync(kFull, in && bin == first_bin)) {
+            if (lane == 0) atomicAdd(hist + bin, 32u);
         } else if (in) {
             atomicAdd(hist + bin, 1u);
         }
@@ -118,17 +103,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     };
     clear();
     for (int base = s0; base < s1; base += 32) {
-        const long long rows = row_of(base + lane);  // of 32 blocks, a lane each
+        const int rows = row_of(base + lane);  // of 32 blocks, a lane each
         const int m = min(32, s1 - base);
         constexpr int kAhead = 8;
         for (int j = 0; j < m; j += kAhead) {
             float x[kAhead];
-            bool ok[kAhead];
+            unsigned ok = 0;
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const long long row = __shfl_sync(kFull, rows, (j + u) & 31);
-                ok[u] = j + u < m && inside((base + j + u) * 32 + lane);
-                x[u] = ok[u] && row >= 0 ? load(scores + row + lane) : __uint_as_float(0x7fc00000);  // a NaN
+                const int row = __shfl_sync(kFull, rows, (j + u) & 31), key = (first + base + j + u) * 32 + lane;
+                const bool in = j + u < m && key >= lo && key < hi;
+                ok |= unsigned(in) << u;
+                x[u] = in && row >= 0 ? load(scores + row + lane) : __uint_as_float(0x7fc00000);  // a NaN
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -136,25 +122,70 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
                 const unsigned v = ordered(x[u]);
                 const int i = (base + j + u) * 32 + lane;
                 if (i < kCached) cache[i] = v;
-                count(ok[u], v >> 21);
+                count(ok >> u & 1, v >> 21);
             }
         }
     }
     find(21);
     const unsigned top = prefix;
     clear();
-    // the keys of the bin, listed; and counted by the next digit
-    for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
-        const unsigned v = value(i);
-        const bool in = inside(i) && (v & 0xffe00000u) == top;
-        const unsigned those = __ballot_sync(kFull, in);
-        if (!those) continue;
-        unsigned at = 0;
-        if (lane == 0) at = atomicAdd(&listed, unsigned(__popc(those)));
-        at = __shfl_sync(kFull, at, 0) + __popc(those & ((1u << lane) - 1));
-        if (in && at < kListed) list[at] = v;
-        count(in, v >> 10 & 2047);
-    }
+    // Four neighbouring keys per lane, 128 of the warp's stretch at a time, in order: f(index of the first,
+    // their scores, of which of them are of the middle a bit each).  Those not held are read again.
+    auto each = [&](auto f) {
+        for (int i0 = s0 * 32; i0 < s1 * 32; i0 += 128) {
+            const int i = i0 + 4 * lane, key = first * 32 + i;
+            unsigned v[4] = {0u, 0u, 0u, 0u}, in = 0;
+            if (i < s1 * 32) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) in |= unsigned(key + u >= lo && key + u < hi) << u;
+                if (i < kCached) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(cache + i);
+                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                } else if (in) {
+                    const long long row = key_row<kPaged>(p, b, start, key);  // (keys 4 k .. 4 k + 3: on one page)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (row >= 0 && (in >> u & 1)) v[u] = ordered(load(scores + row + u));
+                }
+            }
+            f(i, v, in);
+        }
+    };
+    // one key per bin and lane; where a warp's 128 keys share one, once
+    auto count4 = [&](const unsigned (&v)[4], unsigned in, int shift, unsigned mask) {
+        const unsigned bin = v[0] >> shift & mask, first_bin = __shfl_sync(kFull, bin, 0);
+        const bool same = in == 15 && bin == first_bin && (v[1] >> shift & mask) == bin && (v[2] >> shift & mask) == bin &&
+                          (v[3] >> shift & mask) == bin;
+        if (__all_sync(kFull, same)) {
+            if (lane == 0) atomicAdd(hist + bin, 128u);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (in >> u & 1) atomicAdd(hist + (v[u] >> shift & mask), 1u);
+    };
+    // the keys above the bin are counted, those of the bin listed (with the warp whose stretch they are
+    // of, in place of the digit that they share) and counted by the next digit
+    int above = 0;
+    each([&](int, const unsigned (&v)[4], unsigned in) {
+        unsigned those = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            above += (in >> u & 1) && v[u] >> 21 > top >> 21;
+            those |= unsigned((in >> u & 1) && v[u] >> 21 == top >> 21) << u;
+        }
+        if (!__any_sync(kFull, those != 0)) return;
+        if (those) {
+            unsigned at = atomicAdd(&listed, unsigned(__popc(those)));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (those >> u & 1) {
+                    if (at < kListed) list[at] = (v[u] & 0x1fffff) | unsigned(warp) << 21;
+                    ++at;
+                }
+        }
+        count4(v, those, 10, 2047);
+    });
     find(10);
     const bool all_listed = listed <= kListed;
     const int in_list = int(min(listed, unsigned(kListed)));
@@ -162,21 +193,27 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     clear();
     if (all_listed) {
         for (int i = threadIdx.x; i < in_list; i += kSelThreads)
-            if ((list[i] & 0xfffffc00u) == prefix) atomicAdd(hist + (list[i] & 1023), 1u);
+            if ((list[i] >> 10 & 2047) == (prefix >> 10 & 2047)) atomicAdd(hist + (list[i] & 1023), 1u);
     } else {
-        for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
-            const unsigned v = value(i);
-            count(inside(i) && (v & 0xfffffc00u) == prefix, v & 1023);
-        }
+        each([&](int, const unsigned (&v)[4], unsigned in) {
+            unsigned those = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) those |= unsigned((in >> u & 1) && v[u] >> 10 == prefix >> 10) << u;
+            count4(v, those, 0, 1023);
+        });
     }
     find(0);
-    // keys above `prefix` stay, and the first `left` of those equal to it
-    int above = 0, equal = 0;
-    for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
-        const unsigned v = value(i);
-        const bool in = inside(i);
-        above += in && v > prefix;
-        equal += in && v == prefix;
+    // keys above `prefix` stay, and the first `left` of those equal to it: how many a warp's stretch has of both
+    int equal = 0;
+    if (!all_listed) {
+        above = 0;
+        each([&](int, const unsigned (&v)[4], unsigned in) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                above += (in >> u & 1) && v[u] > prefix;
+                equal += (in >> u & 1) && v[u] == prefix;
+            }
+        });
     }
     above = __reduce_add_sync(kFull, above);
     equal = __reduce_add_sync(kFull, equal);
@@ -184,24 +221,118 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
         warp_n[0][warp] = above;
         warp_n[1][warp] = equal;
     }
+    if (all_listed) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < in_list; i += kSelThreads) {
+            const unsigned v = list[i] & 0x1fffff, w = list[i] >> 21, mark = prefix & 0x1fffff;
+            if (v >= mark) atomicAdd(&warp_n[v == mark][w], 1);
+        }
+    }
     __syncthreads();
-    const bool before = lane < warp;  // of the stretches before
-    int at = __reduce_add_sync(kFull, before ? warp_n[0][lane] : 0), ties = __reduce_add_sync(kFull, before ? warp_n[1][lane] : 0);
-    at += min(ties, int(left));
-    const unsigned below = (1u << lane) - 1;
-    for (int i = s0 * 32 + lane; i < s1 * 32; i += 32) {
-        const bool in = inside(i);
-        const unsigned v = value(i);
-        const unsigned eq = __ballot_sync(kFull, in && v == prefix);
-        const bool stays = in && (v > prefix || (v == prefix && ties + __popc(eq & below) < int(left)));
-        const unsigned st = __ballot_sync(kFull, stays);
-        if (stays) kept[lo + at + __popc(st & below)] = first * 32 + i;
-        at += __popc(st);
-        ties += __popc(eq);
+    const bool before = lane < warp;  // the stretches before
+    int na = __reduce_add_sync(kFull, before ? warp_n[0][lane] : 0), ne = __reduce_add_sync(kFull, before ? warp_n[1][lane] : 0);
+    // a key that stays goes behind all above it in the order, and as many of the equal ones as stay
+    each([&](int i, const unsigned (&v)[4], unsigned in) {
+        int mine = 0;  // the lane's keys above (low half) and equal
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (in >> u & 1) mine += v[u] > prefix ? 1 : v[u] == prefix ? 1 << 16 : 0;
+        int scan = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, scan, o);
+            if (lane >= o) scan += x;
+        }
+        const int all = __shfl_sync(kFull, scan, 31);
+        int a = na + ((scan - mine) & 0xffff), q = ne + ((scan - mine) >> 16);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (!(in >> u & 1) || v[u] < prefix) continue;
+            const bool tie = v[u] == prefix;
+            // (k of them as counted; it can only be others where the scores change while this runs)
+            const unsigned slot = unsigned(a + min(q, int(left)));
+            if ((!tie || q < int(left)) && slot < unsigned(k)) kept[lo + slot] = first * 32 + i + u;
+            a += !tie;
+            q += tie;
+        }
+        na += all & 0xffff;
+        ne += all >> 16;
+    });
+}
+
+// The cache row of kept key i, -1 for a bad page id (flagged) or what is no index.
+template <bool kPaged>
+__device__ __forceinline__ long long row_in(const Params &p, int b, long long start, int i) {
+    if (i < 0 || i >= p.max_len) return -1;
+    const long long row = key_row<kPaged>(p, b, start, i);
+    return row < p.total_tokens ? row : -1;
+}
+// Where sequence b goes: its first row, or -1 (flagged) where it does not fit; `table_out`: 0.
+__device__ __forceinline__ long long first_row_out(const EvictParams &e, int b, int n) {
+    if (e.table_out) return 0;
+    const long long to = e.indptr_out[b], end = e.indptr_out[b + 1];
+    if (to >= 0 && end <= e.rows_out && end - to >= n) return to;
+    raise_flag(e.p, SANTA_ERR_INDPTR);
+    return -1;
+}
+// The row that receives its j-th key, -1 (flagged) for a bad page id.
+__device__ __forceinline__ long long row_out(const EvictParams &e, int b, long long to, int j) {
+    if (!e.table_out) return to + j;
+    const int pg = load(e.table_out + (size_t)b * e.max_pages_out + j / e.page_size_out);
+    if (pg >= 0 && (pg + 1LL) * e.page_size_out <= e.rows_out) return (long long)pg * e.page_size_out + j % e.page_size_out;
+    raise_flag(e.p, SANTA_ERR_INDPTR);
+    return -1;
+}
+
+// kMove: the CTA also moves the rows of its head, 16 bytes per thread, `vecs` threads per row.
+template <bool kPaged, bool kMove>
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams e, int vecs) {
+    const Params &p = e.p;
+    const int kvh = blockIdx.x, b = blockIdx.y;
+    extern __shared__ __align__(16) unsigned char smem[];
+    pdl_wait();
+    pdl_launch_dependents();
+    long long start;
+    const int L = seq_bounds<kPaged>(p, b, &start);
+    select_keys<kPaged>(e, b, kvh, L, start, smem);
+    if constexpr (kMove) {
+        const int n = min(L, e.keep);
+        const long long to = first_row_out(e, b, n);
+        if (n == 0 || to < 0) return;
+        __syncthreads();  // the indices, by all threads
+        const int *kept = e.kept + (size_t(b) * p.Hkv + kvh) * e.keep;
+        const uint4 *k = static_cast<const uint4 *>(p.k), *v = static_cast<const uint4 *>(p.v);
+        uint4 *ko = static_cast<uint4 *>(e.k_out), *vo = static_cast<uint4 *>(e.v_out);
+        constexpr int kAhead = 4;
+        const int vec = threadIdx.x % vecs, step = kSelThreads / vecs;
+        for (int j = threadIdx.x / vecs; j < n; j += step * kAhead) {
+            uint4 x[kAhead], y[kAhead];
+            long long at[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                at[u] = -1;
+                if (j + u * step >= n) continue;
+                const long long from = row_in<kPaged>(p, b, start, kept[j + u * step]);
+                at[u] = row_out(e, b, to, j + u * step);
+                if (from < 0) at[u] = -1;
+                if (at[u] < 0) continue;
+                x[u] = load(k + (from * p.Hkv + kvh) * vecs + vec);
+                y[u] = load(v + (from * p.Hkv + kvh) * vecs + vec);
+                if (e.scores_out && vec == 0)
+                    e.scores_out[size_t(kvh) * e.rows_out + at[u]] = load(e.scores + size_t(kvh) * p.total_tokens + from);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (at[u] >= 0) {
+                    ko[(at[u] * p.Hkv + kvh) * vecs + vec] = x[u];
+                    vo[(at[u] * p.Hkv + kvh) * vecs + vec] = y[u];
+                }
+        }
     }
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveBytes = 96 * 1024;  // of K and V of a head, that its selecting CTA moves itself
 constexpr int kMoveTasks = 256;  // rows of one KV head that a CTA looks up at once
 
 // CTA (x, y): destination rows x * rows .. + rows - 1 of sequence y, all KV heads.
@@ -213,16 +344,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     pdl_wait();
     const int n = min(rows, e.lens_out[b] - j0);
     if (n <= 0) return;
-    long long start = 0, to = 0;
+    long long start = 0;
     if (!kPaged) start = p.kv_indptr[b];
-    if (!e.table_out) {
-        to = e.indptr_out[b];
-        const long long end = e.indptr_out[b + 1];
-        if (to < 0 || end > e.rows_out || end - to < e.lens_out[b]) {
-            raise_flag(p, SANTA_ERR_INDPTR);
-            return;
-        }
-    }
+    const long long to = first_row_out(e, b, e.lens_out[b]);
+    if (to < 0) return;
     const uint4 *k = static_cast<const uint4 *>(p.k), *v = static_cast<const uint4 *>(p.v);
     uint4 *ko = static_cast<uint4 *>(e.k_out), *vo = static_cast<uint4 *>(e.v_out);
     for (int t0 = 0; t0 < n * p.Hkv; t0 += kMoveTasks) {
@@ -230,14 +355,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
         __syncthreads();
         for (int t = threadIdx.x; t < count; t += kMoveThreads) {
             const int h = (t0 + t) % p.Hkv, j = j0 + (t0 + t) / p.Hkv;
-            const long long from = key_row<kPaged>(p, b, start, e.kept[(size_t(b) * p.Hkv + h) * e.keep + j]);
-            long long at = to + j;
-            if (e.table_out) {
-                const int pg = load(e.table_out + (size_t)b * e.max_pages_out + j / e.page_size_out);
-                at = pg < 0 || (pg + 1LL) * e.page_size_out > e.rows_out ? -1
-                                                                         : (long long)pg * e.page_size_out + j % e.page_size_out;
-                if (at < 0) raise_flag(p, SANTA_ERR_INDPTR);
-            }
+            const long long from = row_in<kPaged>(p, b, start, e.kept[(size_t(b) * p.Hkv + h) * e.keep + j]);
+            const long long at = row_out(e, b, to, j);
             const bool ok = from >= 0 && at >= 0;
             src[t] = ok ? from * p.Hkv + h : -1;
             dst[t] = at * p.Hkv + h;
@@ -278,14 +397,22 @@ cudaError_t launch_evict(const EvictParams &e, int dtype, cudaStream_t stream) {
     const dim3 heads(unsigned(p.Hkv), unsigned(p.B));
     const int most_cached = (p.max_len + 31) / 32 * 32;  // of whole blocks
     const size_t smem = kSelSmem - (most_cached < kCached ? size_t(kCached - most_cached) * 4 : 0);
+    const int most = e.keep < p.max_len ? e.keep : p.max_len, vecs = p.D * (dtype == SANTA_BF16 ? 2 : 4) / 16;
+    // A head's CTA moves its rows itself while they are few: the second kernel costs 3 us and a launch on
+    // the host, a CTA moves 512 bytes in 20 to 30 ns (8 heads of 138 rows, 70 KB each: 10.3 us with one kernel,
+    // 11.0 with two; 8 heads of 300 rows, 154 KB each: 15.0 and 13.7).
+    const bool move_too = (long long)most * vecs * 32 <= kMoveBytes;
     auto select = [&](auto kern) {
         const cudaError_t r = ensure_smem(kern, kSelSmem);
-        return r != cudaSuccess ? r : launch_kernel(kern, heads, dim3(kSelThreads), smem, stream, true, 0, false, e);
+        return r != cudaSuccess ? r
+                                : launch_kernel(kern, heads, dim3(kSelThreads), smem, stream, true, 0, false, e, vecs);
     };
-    cudaError_t r = paged ? select(evict_select_kernel<true>) : select(evict_select_kernel<false>);
-    if (r != cudaSuccess) return r;
-    const int most = e.keep < p.max_len ? e.keep : p.max_len;
-    if (most == 0) return cudaSuccess;
+    cudaError_t r;
+    if (move_too)
+        r = paged ? select(evict_select_kernel<true, true>) : select(evict_select_kernel<false, true>);
+    else
+        r = paged ? select(evict_select_kernel<true, false>) : select(evict_select_kernel<false, false>);
+    if (r != cudaSuccess || most == 0 || move_too) return r;
     // as many rows per CTA as leave four CTAs per SM
     int rows = 64;
     while (rows > 1 && (long long)((most + rows - 1) / rows) * p.B < 4 * 152) rows /= 2;
@@ -293,7 +420,6 @@ cudaError_t launch_evict(const EvictParams &e, int dtype, cudaStream_t stream) {
     auto move = [&](auto kern) {
         return launch_kernel(kern, grid, dim3(kMoveThreads), 0, stream, true, 0, false, e, rows);
     };
-    const int vecs = p.D * (dtype == SANTA_BF16 ? 2 : 4) / 16;
     if (vecs == 8) return paged ? move(evict_move_kernel<8, true>) : move(evict_move_kernel<8, false>);
     if (vecs == 16) return paged ? move(evict_move_kernel<16, true>) : move(evict_move_kernel<16, false>);
     return paged ? move(evict_move_kernel<32, true>) : move(evict_move_kernel<32, false>);
