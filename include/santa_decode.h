@@ -618,6 +618,7 @@ typedef struct {
  * that sees no key gives zeros.  Equal calls give equal bits.  Sequences that share
  * different prefixes are calls of their own (on slices of q, page_table, kv_lens, out).
  * Single precision throughout: a weight keeps 24 bits on the tensor cores too.
+ * Supported while Hkv * ceil(rows / 64) * ceil(len / 32) stays below 2^31.
  * Workspace: santa_shared_workspace_size, prepared once by santa_split_workspace_init;
  * rules and the other arguments as for santa_decode_window.
  */
@@ -671,11 +672,11 @@ typedef struct {
  *                 num_pages * page_size == rows_out); NULL: contiguous
  *   kept          device [B][Hkv][sinks + recent + budget] int32: the index that each
  *                 row held before, -1 behind the last
- *   lens_out      device [B] int32
+ *   lens_out      device [B] int32; not pages->kv_lens itself
  * A destination that does not fit (a bad page id, or an indptr_out entry without room)
  * is not written, and raises SANTA_ERR_INDPTR; a key on a bad source page counts as of
  * lowest score and its row is not written.  Rows behind a sequence's last are left as
- * they are.  Two kernels, no workspace.
+ * they are.  One kernel or two, no workspace.
  */
 int santa_evict(const santa_problem *p, const santa_keep *keep, const santa_pages *pages, const void *k, const void *v,
                 const float *scores, const long long *kv_indptr, void *k_out, void *v_out, float *scores_out,

@@ -496,7 +496,7 @@ int santa_key_weights(const santa_problem *p, const santa_pages *pages, const vo
                        dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return SANTA_CUDA_ERROR;
         // One sequence fills prop's walk, and is 1.7 us ahead without a plan; of a batch the host does not
-        // know the lengths (16 of 4096 to 32768 keys: 134 us by prop's walk, 103 by equal shares).
+        // know the lengths (16 of 4096 to 32768 keys: 134 us by prop's walk, 110 by equal shares).
         cudaError_t e;
         if (p->dtype == SANTA_BF16 && p->batch > 1) {
             SplitParams sp = {};
@@ -537,7 +537,7 @@ int santa_evict(const santa_problem *p, const santa_keep *keep, const santa_page
     const bool empty = p->max_len == 0 || p->total_tokens == 0;
     if (!empty && (!k || !v || !scores)) return SANTA_INVALID_ARG;
     if (!empty && sum > 0 && (!k_out || !v_out || k_out == v_out || k_out == v || v_out == k)) return SANTA_INVALID_ARG;
-    if (scores_out && scores_out == scores) return SANTA_INVALID_ARG;
+    if ((scores_out && scores_out == scores) || (pages && pages->kv_lens == lens_out)) return SANTA_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(scores, 4) ||
         !aligned(scores_out, 4) || !aligned(kv_indptr, 8) || !aligned(indptr_out, 8) || !aligned(kept, 4) ||
         !aligned(lens_out, 4))

@@ -11,13 +11,21 @@
 // bf16 (shared_mma_kernel): both products on the tensor cores (tcgen05), 128 rows x 64 keys at a
 // time.  K and V come by TMA through a ring of stages (boxes of 32 rows, so that a block may lie
 // on two pages), S = Q K^T goes to tensor memory, a thread per row reads it, and E goes back to
-// tensor memory as the A operand of E V.  E is split into three bf16 parts by truncation (8 + 8 +
+// the tensor cores as the A operand of E V.  E is split into three bf16 parts by truncation (8 + 8 +
 // 8 bits: exact), so a weight keeps its 24 bits; the parts are multiplied from the smallest on,
 // each block into an accumulator that starts at zero and is added to O in registers by an fp32
 // fma: a chain of thousands of additions on the tensor cores would lose bits to truncation.
 // Two streams of four warps keep the tensor cores fed: while one stream's products run, the other
 // forms weights.  They take two tiles of 128 rows over the same blocks or, with at most 128 rows,
-// the even and the odd blocks of one tile.
+// the even and the odd blocks of one tile.  A block's weights come in two halves of 32 keys, so that
+// the products of the first run while the second is formed; a warp per stream issues its products.
+//
+// 64 sequences of 32 query and 8 KV heads of 128 over 32768 keys (34.4 GFLOP counted once, 68.7 with the
+// parts of E; 134 MB): the whole call takes 85.5 us, of which this kernel has 57; per block of 64 keys
+// and both tiles 3900 cycles, 2370 of them busy on the tensor cores.  It is bound by the chain of a
+// block in each stream (S 1000 cycles after the last weights, first half 950, sums of the block before
+// 850, second half 650, barriers): with two thirds of E V left out the call took no less, without the
+// additions to O 3 us less.
 //
 // Tensor memory of a stream, 256 columns: O in 0 .. D - 1, S in 128 .. 191, the larger parts of E in
 // 192 .. 223 and 224 .. 255; the smallest part has no room there and lies in shared memory.  So S of
@@ -58,7 +66,7 @@ struct MmaGeom {
     static constexpr size_t kLow = size_t(2) * kRows * D * 2;      // [2] tiles of E's smallest part
     static constexpr size_t kStage0 = kLow + size_t(2) * kRows * kKeys * 2;
     static constexpr size_t kBars = kStage0 + size_t(kStages) * 2 * kTile;
-    static constexpr size_t kTotal = kBars + (2 * kStages + 13) * 8 + kStages * 8 + 16;
+    static constexpr size_t kTotal = kBars + (2 * kStages + 12) * 8 + kStages * 8 + 16;
     static_assert(kTotal <= 227 * 1024, "shared memory");
 };
 
@@ -155,8 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Geo::kBars), *empty = full + NS;
     // per stream: S is there; E is there, half by half; O is there; Q is there; all products have ended
     uint64_t *sready = empty + NS, *eready = sready + 2, *oready = eready + 4, *qready = oready + 2, *fin = qready + 2;
-    uint64_t *go = fin + 2;  // stream 0 has its first weights
-    uint2 *valid = reinterpret_cast<uint2 *>(go + 1);  // a stage's keys that count, a bit each
+    uint2 *valid = reinterpret_cast<uint2 *>(fin + 2);  // a stage's keys that count, a bit each
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(valid + NS);
 
     if (threadIdx.x == 0) {
@@ -172,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&qready[t], kRows);
             mbar_init(&fin[t], 1);
         }
-        mbar_init(go, 1);
         fence_barrier_init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -238,16 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __shfl_sync(kFull, ok, 0);
             }
         }
-        if (!ok && lane == 0) {  // the copies in flight land before the CTA ends
+        if (lane == 0) {  // the copies in flight land before the CTA ends, whatever the others did
             const long long t0 = clock64();
-            for (int i = it > NS ? it - NS : 0; i < it - 1; ++i)
+            for (int i = it > NS ? it - NS : 0; i < (ok ? it : it - 1); ++i)
                 while (!mbar_try_wait(&full[i % NS], (i / NS) & 1) && clock64() - t0 < kWaitCycles) {
                 }
         }
     } else if (warp >= 9) {  // products of stream t: the warp as one, an elected lane issues
         const int t = warp - 9;
         bool ok = true;
-        bool gone = false;
         uint32_t phQ = 0, ph = 0;
         constexpr uint32_t kind_s = mma_kind(kRows, kKeys, false), kind_o = mma_kind(kRows, D, true);
         const uint32_t base = tmem + t * 256;
@@ -304,9 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0) {
                 ok = wait(&qready[t], phQ) && arrived(0, false);
                 phQ ^= 1;
-                // stream 1 begins half a block later: in step, each would wait for the pipe that the other uses
-                if (ok && t == 1 && !gone) ok = wait(go, 0);
-                gone = gone || t == 1;
                 if (ok) scores(0);
             }
 #pragma unroll 1
@@ -315,11 +317,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_after_sync();
                 sums(i, 0);
-                if (t == 0 && !gone) {
-                    if (elect_one()) mbar_arrive(go);
-                    gone = true;
-                    __syncwarp();
-                }
                 ok = wait(&eready[2 * t + 1], ph);
                 ph ^= 1;
                 if (!ok) break;
@@ -726,7 +723,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
     }
 }
 
-template <int D>
+template <int D, bool kPaged>
 cudaError_t launch_mma(const SharedParams &sp, cudaStream_t stream) {
     const Params &p = sp.p;
     CUtensorMap maps[2];
@@ -738,20 +735,18 @@ cudaError_t launch_mma(const SharedParams &sp, cudaStream_t stream) {
                        CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorUnknown;
     }
-    auto go = [&](auto kern) {
-        cudaError_t r = ensure_smem(kern, MmaGeom<D>::kTotal);
-        static bool checked = false;  // the streams' registers come out of those the kernel is launched with
-        if (r == cudaSuccess && !checked) {
-            cudaFuncAttributes a;
-            r = cudaFuncGetAttributes(&a, kern);
-            if (r == cudaSuccess && a.numRegs < kLaunchRegs) r = cudaErrorNotSupported;
-            checked = r == cudaSuccess;
-        }
-        if (r != cudaSuccess) return r;
-        return launch_kernel(kern, dim3(unsigned(sp.ctas)), dim3(kThreads), MmaGeom<D>::kTotal, stream, true, 0, false,
-                             maps[0], maps[1], sp);
-    };
-    return p.page_table ? go(shared_mma_kernel<D, true>) : go(shared_mma_kernel<D, false>);
+    auto kern = shared_mma_kernel<D, kPaged>;
+    cudaError_t r = ensure_smem(kern, MmaGeom<D>::kTotal);
+    static bool checked = false;  // the streams' registers come out of those the kernel is launched with
+    if (r == cudaSuccess && !checked) {
+        cudaFuncAttributes a;
+        r = cudaFuncGetAttributes(&a, kern);
+        if (r == cudaSuccess && a.numRegs < kLaunchRegs) r = cudaErrorNotSupported;
+        checked = r == cudaSuccess;
+    }
+    if (r != cudaSuccess) return r;
+    return launch_kernel(kern, dim3(unsigned(sp.ctas)), dim3(kThreads), MmaGeom<D>::kTotal, stream, true, 0, false, maps[0],
+                         maps[1], sp);
 }
 
 template <int D>
@@ -765,7 +760,10 @@ cudaError_t launch_f32(const SharedParams &sp, cudaStream_t stream) {
     return sp.p.page_table ? go(shared_f32_kernel<D, true>) : go(shared_f32_kernel<D, false>);
 }
 
-constexpr int kMinBlocks = 2;  // blocks of keys per CTA, at least
+// Blocks of keys per CTA, at least.  bf16: one leaves no SM to the own keys' kernel, which runs beside
+// (4 sequences, 1000 keys: 16.4 us with 1, 12.3 with 2, 13.2 with 4); fp32 blocks are smaller and take
+// longer (8 sequences, 1023 keys of 64: 11.6 us with 1, 12.9 with 2, 17.8 with 4).
+constexpr int min_blocks(int dtype) { return dtype == SANTA_BF16 ? 2 : 1; }
 
 }  // namespace
 
@@ -774,13 +772,15 @@ cudaError_t launch_shared(SharedParams &sp, int dtype, cudaStream_t stream, cons
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const long long X = (long long)sp.p.Hkv * sp.tiles * sp.nb, most = (X + kMinBlocks - 1) / kMinBlocks;
+    const long long X = (long long)sp.p.Hkv * sp.tiles * sp.nb, least = min_blocks(dtype), most = (X + least - 1) / least;
     if (X > 0x7fffffffLL) return cudaErrorNotSupported;
     const int ctas = sms < kSplitCtaBound ? sms : kSplitCtaBound;
     sp.ctas = most < ctas ? int(most) : ctas;
     record_event(tm.begin, stream);
-    if (dtype == SANTA_BF16)
-        e = sp.p.D == 128 ? launch_mma<128>(sp, stream) : launch_mma<64>(sp, stream);
+    if (dtype == SANTA_BF16 && sp.p.page_table)
+        e = sp.p.D == 128 ? launch_mma<128, true>(sp, stream) : launch_mma<64, true>(sp, stream);
+    else if (dtype == SANTA_BF16)
+        e = sp.p.D == 128 ? launch_mma<128, false>(sp, stream) : launch_mma<64, false>(sp, stream);
     else
         e = sp.p.D == 128 ? launch_f32<128>(sp, stream) : launch_f32<64>(sp, stream);
     record_event(tm.end, stream);

@@ -256,7 +256,9 @@ __device__ __forceinline__ int plan_walk(const SplitParams &sp, SplitShared<NW> 
                 }
             if (size == 0) return -1;
             cta0 = (unsigned(e) - size) * p.Hkv + (blockIdx.x - unsigned(b) * p.Hkv) * size;
-        } else if (sp.beside && heads > gridDim.x && unsigned(most) <= kJoinUnits) {  // whole heads, so many each
+        } else if (sp.beside && heads > gridDim.x && unsigned(most) <= kJoinUnits) {
+            // behind a prefix: many short heads, so whole ones, an equal number each, and nothing is joined
+            // across CTAs (64 sequences of 1 to 512 keys, 8 KV heads: the call 85 us, by equal stretches 90)
             ctas = int(gridDim.x);
             auto first_unit = [&](unsigned head) {
                 const unsigned s = head / p.Hkv;

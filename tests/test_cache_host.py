@@ -129,6 +129,7 @@ def test_evict_refuses(sd):
         assert _evict(sd, **bad) == sd.INVALID_ARG, bad
     for bad in BAD_PAGES:
         assert _evict(sd, pages=_pages(sd, **bad), pages_out=out) == sd.INVALID_ARG, bad
+    assert _evict(sd, pages=_pages(sd, kv_lens=10 * A), pages_out=out) == sd.INVALID_ARG  # lengths in place
     assert _evict(sd, p=_problem(sd, head_dim=96)) == sd.UNSUPPORTED
     assert _evict(sd, p=_problem(sd, batch=0), pages_out=out) == sd.OK
 
