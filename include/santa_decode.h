@@ -633,7 +633,8 @@ int santa_shared_workspace_size(const santa_problem *p, size_t *bytes);
  * row r, with A the softmax of each query head of the group,
  *   scores_out[h][r] = decay * scores[h][r] + sum over the group's heads of A_i,
  * where the last `fresh` keys of a sequence start from 0 (their rows may hold another
- * token's score).  Rows of no sequence are left as they are.  scores may be scores_out,
+ * token's score).  Rows of no sequence are left as they are; of sequences that share a
+ * row (a prefix's) one's score stays, any of them.  scores may be scores_out,
  * or NULL (all start from 0).
  *   q, k given   pass 1 of santa_decode_prop runs first, on workspace; of K alone is read
  *   both NULL    workspace is as santa_prop_pass1 left it for the same problem and

@@ -381,7 +381,8 @@ class Decoder:
                     stream=None) -> torch.Tensor:
         """out [Hkv][total_tokens] = decay * scores + the attention weight that each key receives from the group's
         queries (santa_key_weights); without `out`, scores is updated in place.  The last `fresh` keys of a sequence
-        start from 0.  q and k None: after pass1 and before pass2, from what pass1 left."""
+        start from 0; of sequences that share a row one's score stays.  q and k None: after pass1 and before pass2, from what
+        pass1 left."""
         return self._key_weights(q, k, kv_indptr, None, scores, out, decay, fresh, debug, stream)
 
     def key_weights_paged(self, q, k_pool, page_table, kv_lens, page_size, scores=None, out=None, decay=1.0, fresh=0,

@@ -640,3 +640,55 @@ def test_a_run_of_them_together(dtype, d):
                 held = -(-60 // page)
                 free = torch.cat([free, table[b, held:need]]).contiguous()
                 table[b, held:] = -1
+
+
+def _readme_block(call):
+    import os
+    import re
+
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    return next(b for b in re.findall(r"```python\n(.*?)```", text, re.S) if call in b)
+
+
+def test_readme_steps_as_written():
+    """README's shared step and its eviction, run as they stand there."""
+    B, hq, hkv, d, page_size, prefix_len = 2, 8, 2, 128, 64, 128
+    lens, num_pages, width = [1900, 1500], 96, 40
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    ids = torch.randperm(num_pages, generator=gen, device="cuda").tolist()
+    shared, at, table = ids[:2], 2, []
+    for n in lens:
+        own = -(-n // page_size) - 2
+        table.append(shared + ids[at:at + own] + [-1] * (width - 2 - own))
+        at += own
+    pages_to = [ids[at:at + 21], ids[at + 21:at + 42]]
+    where = [torch.tensor([table[b][i // page_size] * page_size + i % page_size for i in range(n)], device="cuda")
+             for b, n in enumerate(lens)]
+    names = dict(dec=Decoder(B, hq, hkv, d, num_pages * page_size, width * page_size, 256, 1, "bf16"), q=rnd(B, hq, d),
+                 k=rnd(B, hkv, d), v=rnd(B, hkv, d), positions3=_ints([[7, 9], [7, 3], [7, 5]]),
+                 slot_map=torch.stack([w[-1] for w in where]), cos_sin=rope_table(64, d), k_pool=rnd(num_pages * page_size, hkv, d),
+                 v_pool=rnd(num_pages * page_size, hkv, d), page_table=_ints(table), lens_out=_ints(lens), page_size=page_size,
+                 prefix_len=prefix_len, rope_sections=rope_sections, scores=torch.zeros((hkv, num_pages * page_size), device="cuda"),
+                 scores_to=torch.zeros((hkv, num_pages * page_size), device="cuda"), pages_to=_ints(pages_to))
+    raw = {n: names[n].clone() for n in "qkv"}
+    exec(_readme_block("shared_paged"), names)
+    rows = _axes_table(names["cos_sin"], names["positions3"], rope_sections((16, 24, 24)))
+    _close(names["q"], *_rope_reference(raw["q"], None, 0.0, rows, d, False), "q")
+    for b, w in enumerate(where):
+        for h in range(hkv):
+            heads = slice(4 * h, 4 * h + 4)
+            want, tol = _attention_reference(names["q"][b, heads].double(), names["k_pool"][w, h].double(),
+                                             names["v_pool"][w, h].double(), 1 / math.sqrt(d), 2.0 ** -23)
+            assert ((names["out"][b, heads].double() - want).abs() <= tol).all()
+    k0, v0 = names["k_pool"].clone(), names["v_pool"].clone()
+    exec(_readme_block("evict_paged"), names)
+    assert names["lens"].tolist() == [1284, 1284]
+    for b, w in enumerate(where):
+        to = torch.tensor([pages_to[b][i // page_size] * page_size + i % page_size for i in range(1284)], device="cuda")
+        for h in range(hkv):
+            want = _kept(names["scores"][h, w].tolist(), lens[b], 4, 256, 1024)
+            assert names["kept"][b, h].tolist() == want
+            src = w[torch.tensor(want, device="cuda")]
+            assert torch.equal(names["k_pool"][to, h], k0[src, h]) and torch.equal(names["v_pool"][to, h], v0[src, h])
+            assert torch.equal(names["scores_to"][h, to], names["scores"][h, src])
